@@ -561,6 +561,156 @@ wsm_status gemm_chain_status(wsm_stream_t stream, int *failed_task);
 /* Validation only (pure host function, no CUDA calls). */
 wsm_status wsm_chain_validate(const wsm_task *tasks, int n_tasks);
 
+/* ---------------------------------------------------------------- decode-step operators
+ *
+ * What lies between and after the GEMMs of a decode step: writing new tokens
+ * into a paged key-value cache, attention over it, the experts' products of a
+ * mixture-of-experts layer, and the log probabilities of the answer.  (No
+ * counterpart on the pages, which keep to the GEMMs.)  The conventions at the
+ * top of this header hold, and:
+ *  - None of them allocates, synchronises, or keeps state between calls: where
+ *    one needs scratch the caller passes it (any contents; nothing of it has
+ *    to survive the call), so calls on different streams and graphs captured
+ *    on one stream never share any.
+ *  - Strides are in elements and not negative; the last dimension of every
+ *    tensor is contiguous.
+ *  - Index tensors (slots, block_table, lengths, offsets, tokens) live on the
+ *    device, so their values are checked there: an index out of range is left
+ *    out as described at each call, never followed, and recorded for
+ *    wsm_operator_status.
+ *  - Up to 2^30 rows (append, log probabilities: 2^31 - 1); none queues
+ *    nothing. */
+
+enum {
+    WSM_DTYPE_BF16 = 0,
+    WSM_DTYPE_FP16 = 1,
+    WSM_DTYPE_FP32 = 2,
+    WSM_DTYPE_E4M3 = 3  /* 8-bit cache entries, each standing for its value times the cache's scale */
+};
+
+/* A paged cache: num_pages pages of page_size tokens, each token kv_heads keys
+ * and as many values of head_dim elements.  Slot s is token s % page_size of
+ * page s / page_size.  Strides: {page, token of a page, head}, multiples of 16
+ * bytes, so both [page, token, head, dim] and [page, head, token, dim] caches
+ * fit, and K and V may interleave. */
+typedef struct {
+    void *K, *V;             /* device, 16-byte aligned */
+    long long k_strides[3], v_strides[3];
+    long long num_pages;
+    int page_size, kv_heads, head_dim;
+    int dtype;               /* WSM_DTYPE_BF16, _FP16 or _E4M3 */
+    float k_scale, v_scale;  /* e4m3: what a stored 1 stands for; 16-bit: 1 */
+} wsm_kv_cache;
+
+/* New tokens: k and v [tokens, kv_heads, head_dim] with strides {token, head}
+ * (multiples of 16 bytes; slices of a fused qkv projection will do), and the
+ * slot of each. */
+typedef struct {
+    const void *k, *v;
+    long long k_strides[2], v_strides[2];
+    const long long *slots;  /* [tokens]; negative: no place, the row is skipped (padding) */
+    int tokens;
+    int dtype;               /* WSM_DTYPE_BF16 or _FP16; a 16-bit cache has the same */
+} wsm_kv_rows;
+
+/* Write rows into their slots.  e4m3: value / scale rounded to nearest, values
+ * beyond +-448 to +-448.  A slot at or past num_pages * page_size is skipped
+ * and recorded.  Slots of one call must differ from one another: two rows with
+ * one slot leave a mixture of both there (in 16-byte pieces). */
+wsm_status wsm_paged_cache_append(const wsm_kv_cache *cache, const wsm_kv_rows *rows, wsm_stream_t stream);
+
+/* One new token of each of `batch` sequences (at most 4096) attends to its
+ * sequence's tokens in the cache, the new one included (append it first).
+ * Sequence b's token i lies on page block_table[b * table_stride + i /
+ * page_size].  Query heads h * G .. h * G + G - 1 (G = heads / kv_heads, any
+ * whole number) share key-value head h.
+ *     O[b, h, :] = v_scale * sum_j softmax_j(scale * k_scale * q . k_j) v_j
+ * over the last `window` tokens (0: all).  Scores, softmax statistics and sums
+ * in fp32; the softmax weights are rounded to 16 bits for the second product.
+ *  - lengths[b] <= 0: no token; O is zero and lse -infinity.  The same where
+ *    every score is -infinity.
+ *  - A length past max_pages * page_size is taken as that, and recorded.
+ *  - A page number outside [0, num_pages) within a sequence's length: its
+ *    tokens are left out, and that is recorded.  Entries past a sequence's last
+ *    page are not read, nor are cache slots past its length.
+ *  - head_dim 64, 96, 128 or 256.  Results do not depend on timing. */
+typedef struct {
+    const void *Q;           /* [batch, heads, head_dim], strides {sequence, head}, multiples of 16 bytes */
+    void *O;                 /* the same shape; its own strides */
+    float *lse;              /* [batch, heads] natural logarithm of the softmax's sum, or NULL */
+    const int *block_table;  /* [batch, max_pages] */
+    const int *lengths;      /* [batch] */
+    long long q_strides[2], o_strides[2];
+    long long table_stride;
+    void *workspace;         /* device, 16-byte aligned, wsm_paged_attention_workspace_bytes */
+    size_t workspace_bytes;
+    int batch, heads, max_pages;
+    int window;              /* 0: no window */
+    int dtype;               /* of Q and O: WSM_DTYPE_BF16 or _FP16; a 16-bit cache has the same */
+    float scale;
+} wsm_attention;
+size_t wsm_paged_attention_workspace_bytes(int batch, int head_dim);  /* current device; 0 on error */
+wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *args, wsm_stream_t stream);
+
+/* Products grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of X belong
+ * to expert e, any number of them, none included:
+ *     Y[r, n] = scale_r * sum_k X[r, k] * W[e, n, k],   scale_r = row_scale[r] or 1.
+ * WSM_EPI_SILU_MUL takes W's gate and up rows in alternating blocks of 8 as
+ * skinny_gemm_ex does (N a multiple of 16) and gives silu(G) * U [rows, N / 2],
+ * row_scale applied last.  fp32 accumulation, one rounding of the result.
+ *  - K >= 8 and K % 8 == 0, N >= 1, experts <= 1024.
+ *  - Rows before offsets[0] or from offsets[experts] on are left as they were.
+ *  - offsets are read clamped to [0, rows] and never falling (an offset below
+ *    an earlier one is taken as that one); what had to be mended is recorded.
+ *  - Tiles cut across CTAs are added in K order: results do not depend on timing. */
+typedef struct {
+    const void *X;           /* [rows, K], 16-byte aligned */
+    const void *W;           /* [experts, N, K], 16-byte aligned */
+    void *Y;                 /* [rows, N], or [rows, N / 2] with WSM_EPI_SILU_MUL */
+    const int *offsets;      /* [experts + 1] */
+    const float *row_scale;  /* [rows], or NULL */
+    long long x_stride;      /* between rows; X and W strides multiples of 16 bytes */
+    long long w_strides[2];  /* {expert, row} */
+    long long y_stride;
+    void *workspace;         /* device, 16-byte aligned, wsm_expert_gemm_workspace_bytes */
+    size_t workspace_bytes;
+    int rows, experts, N, K;
+    int epilogue;            /* WSM_EPI_NONE or WSM_EPI_SILU_MUL */
+    int dtype;               /* X, W and Y: WSM_DTYPE_BF16 or _FP16 */
+} wsm_experts;
+size_t wsm_expert_gemm_workspace_bytes(int rows, int experts);  /* current device; 0 on error */
+wsm_status wsm_expert_gemm(const wsm_experts *args, wsm_stream_t stream);
+
+/* Per row of logits [rows, vocab]: the log probability of a given token, the
+ * entropy of the row's distribution (natural logarithms) and its `top` likeliest
+ * tokens (at most 32) with their log probabilities, likeliest first, equal ones
+ * by the lower index -- in one pass over the logits.
+ *  - A token below 0 asks for nothing: its logprob is 0 (padding).  A token at
+ *    or past vocab gives NaN and is recorded.
+ *  - Logits of -infinity have probability 0; they are never among the
+ *    alternatives, whose missing places hold id -1 and -infinity.  A row with
+ *    nothing else: logprob -infinity, entropy 0.
+ *  - A NaN or +infinity in a row makes its logprob (of a token asked for),
+ *    entropy and alternatives NaN, with ids -1. */
+typedef struct {
+    const void *logits;      /* [rows, vocab], element-aligned */
+    const long long *tokens; /* [rows], or NULL: none asked for */
+    float *logprob;          /* [rows], or NULL */
+    float *entropy;          /* [rows], or NULL */
+    long long *top_ids;      /* [rows, top], or NULL when top = 0 */
+    float *top_logprobs;     /* [rows, top], or NULL when top = 0 */
+    long long stride;        /* between rows of logits */
+    int rows, vocab, top;
+    int dtype;               /* WSM_DTYPE_FP32, _BF16 or _FP16 */
+} wsm_logprobs;
+wsm_status wsm_token_logprobs(const wsm_logprobs *args, wsm_stream_t stream);
+
+/* Synchronise `stream`, then report what the operators above recorded on the
+ * current device, on any stream, since the last check, and clear it:
+ * WSM_ERR_INVALID for an index out of range, WSM_ERR_TIMEOUT for a device-side
+ * wait that ran out (*code the same; message in wsm_last_error()), else WSM_OK. */
+wsm_status wsm_operator_status(wsm_stream_t stream, int *code);
+
 /* ---------------------------------------------------------------- misc */
 
 /* Message of the last error on this host thread ("" when none). */

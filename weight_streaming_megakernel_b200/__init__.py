@@ -24,6 +24,7 @@ __all__ = [
     "workspace_bytes", "stream_status", "Task", "Chain", "gemm_chain", "chain_validate", "chain_plan", "last_error",
     "skinny_gemm_noalloc", "workspace_status", "gemm_chain_status", "debug_stall", "sm_die_map",
     "abi_version", "HEADER_SYMBOLS",
+    "paged_cache_append", "paged_attention", "expert_gemm", "token_logprobs", "TokenLogprobs", "operator_status",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libwsm.so")
@@ -49,6 +50,8 @@ HEADER_SYMBOLS = (
     "wsm_chain_trace",
     "wsm_chain_destroy",
     "gemm_chain", "wsm_chain_validate", "wsm_last_error", "wsm_abi_version",
+    "wsm_paged_cache_append", "wsm_paged_attention_workspace_bytes", "wsm_paged_attention",
+    "wsm_expert_gemm_workspace_bytes", "wsm_expert_gemm", "wsm_token_logprobs", "wsm_operator_status",
 )
 
 
@@ -158,6 +161,21 @@ def lib() -> ctypes.CDLL:
         L.wsm_chain_plan.restype = st
         L.wsm_chain_validate.argtypes = [ctypes.POINTER(_Task), i]
         L.wsm_chain_validate.restype = st
+        # the decode-step operators take their argument structs as packed bytes (operators.py)
+        L.wsm_paged_cache_append.argtypes = [vp, vp, vp]
+        L.wsm_paged_cache_append.restype = st
+        L.wsm_paged_attention.argtypes = [vp, vp, vp]
+        L.wsm_paged_attention.restype = st
+        L.wsm_paged_attention_workspace_bytes.argtypes = [i, i]
+        L.wsm_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.wsm_expert_gemm.argtypes = [vp, vp]
+        L.wsm_expert_gemm.restype = st
+        L.wsm_expert_gemm_workspace_bytes.argtypes = [i, i]
+        L.wsm_expert_gemm_workspace_bytes.restype = ctypes.c_size_t
+        L.wsm_token_logprobs.argtypes = [vp, vp]
+        L.wsm_token_logprobs.restype = st
+        L.wsm_operator_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
+        L.wsm_operator_status.restype = st
         L.wsm_last_error.argtypes = []
         L.wsm_last_error.restype = ctypes.c_char_p
         L.wsm_abi_version.argtypes = []
@@ -508,3 +526,7 @@ def gemm_chain(tasks: Sequence[Task], stream=None):
     """One-shot chain run (prepared chains are cached by the library)."""
     arr = _tasks_array(tasks)
     _check(lib().gemm_chain(arr, len(tasks), _stream_handle(stream)), "gemm_chain")
+
+
+from .operators import (TokenLogprobs, expert_gemm, operator_status, paged_attention,  # noqa: E402
+                        paged_cache_append, token_logprobs)

@@ -1136,6 +1136,34 @@ wsm_status plan_chain(const wsm_task *tasks, int n, const wsm_chain_opts *opts, 
 namespace wsm {
 // Sets the message wsm_last_error() returns on this host thread.
 void set_last_error_message(const char *msg) { g_err = msg ? msg : ""; }
+
+// For the operators of the other source files (wsm_ops.cuh).
+unsigned long long take_launch_stall() { return take_stall(); }
+
+wsm_status device_sms(int *dev, int *sms) {
+    WSM_CUDA(cudaGetDevice(dev));
+    DevInfo *d;
+    wsm_status st = dev_info(*dev, &d);
+    if (st == WSM_OK) *sms = d->sms;
+    return st;
+}
+
+wsm_status encode_tiled(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
+                        const cuuint64_t *strides, const cuuint32_t *box) {
+    EncodeTiledFn enc;
+    wsm_status st = get_encode(&enc);
+    if (st != WSM_OK) return st;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = enc(map, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(WSM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return WSM_OK;
+}
+
+wsm_status cache_status_ptr(void **p);     // wsm_cache.cu
+wsm_status experts_status_ptr(void **p);   // wsm_experts.cu
+wsm_status logprobs_status_ptr(void **p);  // wsm_logprobs.cu
 }  // namespace wsm
 
 using namespace wsm;
@@ -1293,6 +1321,32 @@ wsm_status wsm_workspace_status(const void *workspace, size_t workspace_bytes, w
     if (h[0] == 0) return WSM_OK;
     if (code) *code = h[0];
     return fail(WSM_ERR_TIMEOUT, "device-side wait ran out in a call on this workspace (cta %d, site %d)", h[2], h[3]);
+}
+
+wsm_status wsm_operator_status(wsm_stream_t stream_, int *code) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (code) *code = 0;
+    static wsm_status (*const blocks[])(void **) = {cache_status_ptr, experts_status_ptr, logprobs_status_ptr};
+    static const char *const names[] = {"the paged cache or its attention", "the expert products", "the log probabilities"};
+    int first[kStatusWords] = {};
+    int which = 0;
+    for (int i = 0; i < 3; ++i) {
+        void *ptr = nullptr;
+        wsm_status st = blocks[i](&ptr);
+        if (st != WSM_OK) return st;
+        int h[kStatusWords] = {};
+        if ((st = read_clear_status(ptr, stream, h)) != WSM_OK) return st;
+        if (h[0] != 0 && first[0] == 0) {
+            memcpy(first, h, sizeof h);
+            which = i;
+        }
+    }
+    if (first[0] == 0) return WSM_OK;
+    if (code) *code = first[0];
+    if (first[0] == WSM_ERR_TIMEOUT)
+        return fail(WSM_ERR_TIMEOUT, "device-side wait ran out in %s (cta %d, site %d)", names[which], first[2], first[3]);
+    return fail(WSM_ERR_INVALID, "an index out of range in %s (row, sequence or expert %d, site %d)", names[which], first[1],
+                first[3]);
 }
 
 wsm_status wsm_debug_stall(int calls, unsigned long long limit_ns) {

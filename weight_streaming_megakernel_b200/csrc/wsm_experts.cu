@@ -1,0 +1,620 @@
+// wsm_experts.cu -- matrix products grouped by expert with ragged row counts (wsm_expert_gemm): the gate+up
+// and down projections of a mixture-of-experts layer, for one token to whole prompts.
+//
+//     Y[r, n] = scale_r * sum_k X[r, k] * W[e, n, k]      for the rows r of expert e
+//
+// What bounds it: with few rows to an expert, reading the weights of the experts that have any (2 N K bytes
+// against 2 m N K operations: under about 250 rows each); with more, the tensor cores.  Both want the same
+// layout, the product transposed: 128 rows of W are the MMA's M side and an expert's rows its N side, which may
+// be any multiple of 16 up to 256, so a handful of rows wastes little and a prompt's fill the instruction.
+//
+//   experts_plan_kernel (one block) reads the offsets, cuts every expert's product into tiles of 128 weight
+//   rows x up to 256 rows of X (an expert's rows cut evenly), and few or last tiles along K into units; it
+//   clears the claim and arrival counters of this call.  So nothing outlives a call and nothing needs to have
+//   been cleared before.
+//   experts_kernel (persistent, one CTA per SM) claims units in order -- SMs do not stream at one rate -- and
+//   runs them: warp 0 loads by TMA into a ring of four 48 KB stages, warp 1 issues tcgen05.mma into one of two
+//   accumulators in tensor memory, warps 2-5 take finished ones out: activation, scale, rounding, stores.  A
+//   tile cut along K leaves fp32 partials, which its last unit to finish adds in K order, so results do not
+//   depend on which SM ran what.
+#include "wsm_ops.cuh"
+#include "wsm_tcgen05.cuh"
+
+#include <algorithm>
+
+namespace wsm {
+
+namespace {
+
+static __device__ int g_experts_status[kOpStatusInts];
+
+constexpr int kMaxExperts = 1024;
+constexpr int kTileN = 128;         // weight rows per tile (MMA M)
+constexpr int kTileRows = 256;      // most rows of X per tile (MMA N)
+constexpr int kBK = 64;             // K elements per box (a 128-byte swizzle row)
+constexpr int kStageBytes = 48 * 1024;
+constexpr int kStages = 4;
+constexpr int kBoxW = kTileN * kBK * 2;
+constexpr int kNarrow = 64;         // up to this many rows a stage holds two K boxes, above one
+constexpr int kNarrowX = kNarrow * kBK * 2;
+constexpr int kXMaps = 5;           // boxes of 256, 128, 64, 32 and 16 rows
+constexpr int kExThreads = 192;
+constexpr uint32_t kExTmemCols = 2 * kTileRows;
+constexpr int kLead = 2;            // a CTA claims its next unit this many stages before its unit ends
+constexpr unsigned long long kExWaitNs = 4000000000ull;
+
+// One expert's part of the plan.
+struct ExpertRec {
+    int lo, m;                      // its rows
+    int tile0, unit0;               // tiles and units of the experts before it
+    int part0;                      // its first partial, in blocks of 16 rows x 128
+    int nu, ku;                     // units of each split tile, K boxes of a unit
+    int mrows;                      // rows per tile, a multiple of 16
+};
+// Head of the scratch: [0] units, [1] tiles before the split ones, [2] claim counter, [3] experts that have rows + 1 ...
+enum : int { kHdrUnits = 0, kHdrHead = 1, kHdrClaim = 2 };
+constexpr int kHdrBytes = 256;
+
+struct ExpertParams {
+    CUtensorMap tmW;                // [experts][N][K], box 128 x 64
+    CUtensorMap tmX[kXMaps];        // [rows][K], boxes 256 >> i rows x 64
+    void *Y;
+    const int *offsets;
+    const float *row_scale;
+    long long y_stride;
+    int *hdr;
+    ExpertRec *rec;                 // [experts + 1]
+    unsigned int *tile_cnt;         // arrival counters of the split tiles
+    float *part;
+    int part_cap;                   // partial blocks there is room for
+    int cnt_cap;
+    int rows, experts, N, K;
+    int kb;                         // K boxes
+    int n_g;                        // tiles along N
+    int silu;
+    int sms;
+    uint32_t idesc;                 // MMA descriptor without its N
+    unsigned long long stall_ns;
+};
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Tiles along an expert's rows, and the rows of each (cut evenly, a multiple of 16).
+__device__ __forceinline__ int m_tiles_of(int m) { return ceil_div(m, kTileRows); }
+
+// ------------------------------------------------------------------ plan
+
+template <bool kMax> __device__ __forceinline__ int block_scan(int v, int *warp_tot) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (int)blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = kMax ? max(v, u) : v + u;
+    }
+    __syncthreads();                                    // (the array may still be read from the scan before)
+    if (lane == 31) warp_tot[warp] = v;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warps; ++w)
+        if (w < warp) before = kMax ? max(before, warp_tot[w]) : before + warp_tot[w];
+    return kMax ? max(before, v) : before + v;
+}
+
+__global__ void __launch_bounds__(kMaxExperts) experts_plan_kernel(const __grid_constant__ ExpertParams p) {
+    __shared__ int warp_tot[32];
+    __shared__ int tiles_all;
+    const int e = threadIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = e; i < p.cnt_cap; i += blockDim.x) p.tile_cnt[i] = 0u;
+    // offsets: into [0, rows], never falling
+    const bool have = e < p.experts;
+    const int raw0 = p.offsets[0];
+    const int raw = have ? p.offsets[e + 1] : 0;
+    const int lo0 = min(max(raw0, 0), p.rows);
+    const int top = have ? min(max(raw, lo0), p.rows) : 0;
+    const int hi = max(block_scan<true>(top, warp_tot), lo0);
+    int lo = __shfl_up_sync(0xffffffffu, hi, 1);
+    if ((e & 31) == 0) {
+        lo = lo0;
+        for (int w = 0; w < (e >> 5); ++w) lo = max(lo, warp_tot[w]);
+    }
+    if (have && (raw != hi || (e == 0 && raw0 != lo0))) record_op_error(g_experts_status, kCodeInvalid, e, kSiteOffsets);
+    const int m = have ? hi - lo : 0;
+    const int mt = m_tiles_of(m);
+    const int tiles = mt * p.n_g;
+    const int tile_end = block_scan<false>(tiles, warp_tot);
+    if (e == (int)blockDim.x - 1) tiles_all = tile_end;
+    __syncthreads();
+    const int total = tiles_all;
+    // Few tiles: all are cut so that each SM gets about three units.  Many: whole tiles, and the last one per
+    // SM cut in two, so that the SMs end together.  A unit is long against its partial sums' way out and back.
+    const int head = total >= 3 * p.sms ? total - p.sms : 0;
+    const int want = total >= 3 * p.sms ? 2 : ceil_div(3 * p.sms, max(total, 1));
+    const int mrows = mt > 0 ? ceil_div(ceil_div(m, mt), 16) * 16 : 16;
+    const int least = mrows <= 64 ? 8 : mrows <= 128 ? 16 : 32;
+    int nu = max(1, min(want, p.kb / least));
+    const int whole = min(max(head - (tile_end - tiles), 0), tiles);   // tiles of this expert that stay whole
+    int ku = ceil_div(p.kb, nu);
+    nu = ceil_div(p.kb, ku);
+    const int blocks = nu > 1 ? (tiles - whole) * nu * (mrows / 16) : 0;
+    const int part_end = block_scan<false>(min(blocks, p.part_cap + 1), warp_tot);
+    if (nu > 1 && (blocks > p.part_cap || part_end > p.part_cap)) {    // no room for its partials: whole tiles
+        nu = 1;
+        ku = p.kb;
+    }
+    const int units = whole + (tiles - whole) * nu;
+    const int unit_end = block_scan<false>(units, warp_tot);
+    if (have) {
+        ExpertRec r;
+        r.lo = lo;
+        r.m = m;
+        r.tile0 = tile_end - tiles;
+        r.unit0 = unit_end - units;
+        r.part0 = part_end - blocks;
+        r.nu = nu;
+        r.ku = ku;
+        r.mrows = mrows;
+        p.rec[e] = r;
+    }
+    if (e == (int)blockDim.x - 1) {
+        p.hdr[kHdrUnits] = unit_end;
+        p.hdr[kHdrHead] = head;
+        p.hdr[kHdrClaim] = 0;
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+// A unit: K boxes k0 .. k1 - 1 of one tile.
+struct Unit {
+    int expert, n0;                 // weight rows n0 .. n0 + 127 of the expert
+    int row0, rows;                 // rows of X in the tile
+    int mrows;
+    int k0, k1;
+    int nu, part;                   // units of its tile, and the first one's partial block
+    int split;                      // index of its tile among the split ones
+    int j;                          // which of the tile's units
+};
+
+// (unit0 of the experts in shared memory: the last expert whose first unit is not past u has it -- experts
+// without rows share their successor's unit0 and come before it)
+__device__ __forceinline__ Unit unit_at(const ExpertParams &p, const int *unit0, int head, int u) {
+    int lo = 0, hi = p.experts - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (unit0[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    const ExpertRec r = p.rec[lo];
+    const int v = u - r.unit0;
+    const int mt = m_tiles_of(r.m);
+    const int whole = min(max(head - r.tile0, 0), mt * p.n_g);
+    Unit t;
+    t.expert = lo;
+    int tile;
+    if (v < whole) {
+        tile = v;
+        t.nu = 1;
+        t.j = 0;
+        t.k0 = 0;
+        t.k1 = p.kb;
+        t.part = t.split = 0;
+    } else {
+        const int s = (v - whole) / r.nu;
+        tile = whole + s;
+        t.nu = r.nu;
+        t.j = v - whole - s * r.nu;
+        t.k0 = t.j * r.ku;
+        t.k1 = min(p.kb, t.k0 + r.ku);
+        t.part = r.part0 + s * r.nu * (r.mrows / 16);
+        t.split = r.tile0 + tile - head;
+    }
+    // tiles of one weight column next to one another: they run at the same time and share it in L2
+    const int g = tile / mt, i = tile - g * mt;
+    t.n0 = g * kTileN;
+    t.mrows = r.mrows;
+    t.row0 = r.lo + i * r.mrows;
+    t.rows = min(r.mrows, r.m - i * r.mrows);
+    return t;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y,
+                                               uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+
+// Outputs of one thread: weight row n, rows row0 .. row0 + cnt - 1 of X, sums v.  With SiLU*mul the up value
+// of gate row n comes from the thread of row n + 8 (lane ^ 8); every lane of the warp calls this alike.
+template <typename T>
+__device__ __forceinline__ void emit_rows(const ExpertParams &p, int n, int row0, int cnt, const float (&v)[16]) {
+    T *Y = reinterpret_cast<T *>(p.Y);
+    const int col = p.silu ? ((n >> 4) << 3) + (n & 7) : n;
+    const bool writer = n < p.N && !(p.silu && (n & 8));
+    T *y = Y + (long long)row0 * p.y_stride + col;
+    float s[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = (p.row_scale && i < cnt) ? p.row_scale[row0 + i] : 1.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (i >= cnt) break;                            // uniform across the warp
+        float x = v[i];
+        if (p.silu) {
+            const float up = __shfl_xor_sync(0xffffffffu, x, 8);
+            x = x / (1.f + expf(-x)) * up;
+        }
+        if (writer) y[i * p.y_stride] = from_f32<T>(x * s[i]);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_constant__ ExpertParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_dyn[];
+    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], accf_bar[2], acce_bar[2], drain_bar;
+    __shared__ int stage_meta[kStages][4];              // {unit, first / last / done, MMA N, K boxes}
+    __shared__ int acc_meta[2];                         // unit, or -1 at the end
+    __shared__ int unit0[kMaxExperts];
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ volatile int abort_flag;
+    __shared__ int last_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    int *const status = g_experts_status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf_bar[b], 2);                 // tcgen05.commit and the MMA thread's unit number
+            mbar_init(&acce_bar[b], 4);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&p.tmW);
+    }
+    if (warp == 1) tmem_alloc(&tmem_base_sh, kExTmemCols);
+    pdl_wait();                                         // the plan is there, and whatever came before it
+    pdl_launch_dependents();
+    for (int e = threadIdx.x; e < p.experts; e += kExThreads) unit0[e] = p.rec[e].unit0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_base_sh;
+    const int n_units = p.hdr[kHdrUnits], head = p.hdr[kHdrHead];
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_normal();
+            int s = 0;
+            uint32_t ph = 0;
+            long long issued = 0;
+            bool aborted = false;
+            if (p.stall_ns && blockIdx.x == 0) {
+                // test hook: wait, bounded, on a word nothing sets, then abandon this CTA's work
+                const unsigned long long t0 = globaltimer();
+                while (ld_acquire_gpu(reinterpret_cast<const unsigned int *>(&status[kStatusStallFlag])) == 0u &&
+                       globaltimer() - t0 <= p.stall_ns)
+                    __nanosleep(256);
+                record_op_error(status, kCodeTimeout, -1, kSiteStall);
+                abort_flag = 1;
+                aborted = true;
+            }
+            int u = (int)blockIdx.x;
+            while (!aborted && u < n_units) {
+                const Unit t = unit_at(p, unit0, head, u);
+                const bool narrow = t.mrows <= kNarrow;
+                const int step = narrow ? 2 : 1;
+                // weights with one reader leave L2 first
+                const uint64_t pol_w = p.rec[t.expert].m <= kTileRows ? pol_once : pol_keep;
+                int next = n_units;
+                bool claimed = false;
+                for (int k = t.k0; k < t.k1; k += step) {
+                    if (!mbar_wait_bounded(&empty_bar[s], ph ^ 1, &abort_flag, kExWaitNs, status, t.expert, kSiteEmpty)) {
+                        aborted = true;
+                        break;
+                    }
+                    const int boxes = min(step, t.k1 - k);
+                    stage_meta[s][0] = u;
+                    stage_meta[s][1] = (k == t.k0 ? kMetaFirst : 0) | (k + step >= t.k1 ? kMetaLast : 0);
+                    stage_meta[s][2] = t.mrows;
+                    stage_meta[s][3] = boxes;
+                    mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(boxes * (kBoxW + t.mrows * kBK * 2)));
+                    const uint32_t st = smem_u32(ring + (size_t)s * kStageBytes);
+                    for (int b = 0; b < boxes; ++b) {
+                        tma_load_3d(st + b * kBoxW, &p.tmW, &full_bar[s], (k + b) * kBK, t.n0, t.expert, pol_w);
+                        uint32_t xd = st + step * kBoxW + b * kNarrowX;
+                        int at = t.row0, left = t.mrows;
+                        for (int i = 0; i < kXMaps; ++i) {
+                            const int h = kTileRows >> i;
+                            if (left >= h) {
+                                tma_load_2d_at(xd, &p.tmX[i], &full_bar[s], (k + b) * kBK, at, pol_keep);
+                                xd += (uint32_t)(h * kBK * 2);
+                                at += h;
+                                left -= h;
+                            }
+                        }
+                    }
+                    ++issued;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    if (!claimed && t.k1 - k <= kLead * step) {
+                        next = (int)gridDim.x + (int)atom_add_relaxed_gpu(reinterpret_cast<unsigned int *>(&p.hdr[kHdrClaim]), 1u);
+                        claimed = true;
+                    }
+                }
+                u = next;
+            }
+            // every copy has landed before the CTA ends
+            drain_issued(full_bar, kStages, issued, kExWaitNs, status);
+            if (!aborted && mbar_wait_bounded(&empty_bar[s], ph ^ 1, &abort_flag, kExWaitNs, status, -1, kSiteEmpty)) {
+                stage_meta[s][1] = kMetaDone;
+                mbar_arrive(&full_bar[s]);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, acc_i = 0;
+            int buf = 0;
+            bool any = false;
+            for (;;) {
+                if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag, kExWaitNs, status, -1, kSiteFull)) break;
+                tc_fence_after();
+                const int unit = stage_meta[s][0], flags = stage_meta[s][1], mrows = stage_meta[s][2], boxes = stage_meta[s][3];
+                if (flags & (kMetaFirst | kMetaDone)) {
+                    buf = (int)(acc_i & 1u);
+                    if (!mbar_wait_bounded(&acce_bar[buf], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc)) break;
+                    tc_fence_after();
+                }
+                if (flags & kMetaDone) {
+                    acc_meta[buf] = -1;
+                    mbar_arrive(&accf_bar[buf]);
+                    mbar_arrive(&accf_bar[buf]);
+                    break;
+                }
+                const uint32_t idesc = p.idesc | ((uint32_t)(mrows >> 3) << 17);
+                const uint32_t d = tmem_base + (uint32_t)(buf * kTileRows);
+                const uint32_t st = smem_u32(ring + (size_t)s * kStageBytes);
+                const uint32_t x0 = st + (mrows <= kNarrow ? 2 : 1) * kBoxW;
+                for (int b = 0; b < boxes; ++b) {
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k)
+                        tc_mma(d, sw128_desc(st + b * kBoxW + 32u * k), sw128_desc(x0 + b * kNarrowX + 32u * k), idesc,
+                               ((flags & kMetaFirst) && b == 0 && k == 0) ? 0u : 1u);
+                }
+                any = true;
+                tc_commit(&empty_bar[s]);
+                if (flags & kMetaLast) {
+                    acc_meta[buf] = unit;
+                    mbar_arrive(&accf_bar[buf]);
+                    tc_commit(&accf_bar[buf]);
+                    ++acc_i;
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            if (any) {
+                // all MMAs are complete before tensor memory is released
+                tc_commit(&drain_bar);
+                volatile int never = 0;
+                mbar_wait_bounded(&drain_bar, 0, &never, kExWaitNs, status, -1, kSiteDrain);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;                         // TMEM lane quadrant this warp may read
+        const int row = q * 32 + lane;                  // weight row within the tile
+        const bool leader = threadIdx.x == 64;
+        for (uint32_t i = 0;; ++i) {
+            const int buf = (int)(i & 1u);
+            const bool ab = !mbar_wait_bounded(&accf_bar[buf], (i >> 1) & 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc);
+            const int u = ab ? -1 : acc_meta[buf];
+            if (vote_or(u < 0, 1, 128)) break;          // the four warps stop together
+            tc_fence_after();
+            const Unit t = unit_at(p, unit0, head, u);
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTileRows);
+            float *part = p.part + ((size_t)t.part + (size_t)t.j * (t.mrows / 16)) * (16 * kTileN) + row;
+#pragma unroll 1
+            for (int c = 0; c < t.rows; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(taddr + (uint32_t)c, r);
+                tmem_ld_wait16(r);
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+                if (t.nu == 1) {
+                    emit_rows<T>(p, t.n0 + row, t.row0 + c, min(16, t.rows - c), v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (c + k < t.rows) part[(size_t)(c + k) * kTileN] = v[k];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acce_bar[buf]);
+            if (t.nu == 1) continue;
+            // the tile's last unit to arrive adds all partials, in K order
+            named_bar_sync(2, 128);
+            if (leader) last_flag = atom_add_acqrel_gpu(&p.tile_cnt[t.split], 1u) == (unsigned int)(t.nu - 1) ? 1 : 0;
+            named_bar_sync(2, 128);
+            if (!last_flag) continue;
+            const float *from = p.part + (size_t)t.part * (16 * kTileN) + row;
+            const size_t step = (size_t)(t.mrows / 16) * (16 * kTileN);
+#pragma unroll 1
+            for (int c = 0; c < t.rows; c += 16) {
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = 0.f;
+                for (int j = 0; j < t.nu; ++j) {
+                    float w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) w[k] = c + k < t.rows ? ld_cg_f32(from + j * step + (size_t)(c + k) * kTileN) : 0.f;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = j == 0 ? w[k] : v[k] + w[k];
+                }
+                emit_rows<T>(p, t.n0 + row, t.row0 + c, min(16, t.rows - c), v);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, kExTmemCols);
+}
+
+// ------------------------------------------------------------------ host side
+
+struct ExLayout {
+    size_t rec, cnt, part, total;
+    int cnt_cap, part_cap;
+};
+ExLayout experts_layout(int rows, int experts, int sms) {
+    ExLayout l;
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    const int mrows = (std::min(rows, kTileRows) + 15) / 16 * 16;
+    l.cnt_cap = 3 * sms;                                // split tiles: fewer than three per SM
+    // units of split tiles: under six per SM; at most 32 MB of partials (tiles that find no room stay whole)
+    l.part_cap = std::min(6 * sms * (mrows / 16), 4096);
+    l.rec = kHdrBytes;
+    l.cnt = up(l.rec + sizeof(ExpertRec) * (size_t)experts);
+    l.part = up(l.cnt + 4 * (size_t)l.cnt_cap);
+    l.total = l.part + (size_t)l.part_cap * (16 * kTileN * 4);
+    return l;
+}
+
+}  // namespace
+
+wsm_status experts_status_ptr(void **p) {
+    WSM_OP_CUDA(cudaGetSymbolAddress(p, g_experts_status));
+    return WSM_OK;
+}
+
+}  // namespace wsm
+
+using namespace wsm;
+
+extern "C" {
+
+size_t wsm_expert_gemm_workspace_bytes(int rows, int experts) {
+    if (rows < 0 || experts < 1 || experts > kMaxExperts) {
+        op_fail(WSM_ERR_UNSUPPORTED, "expert products take up to %d experts and no negative rows (got %d, %d)", kMaxExperts, experts, rows);
+        return 0;
+    }
+    int dev, sms;
+    if (device_sms(&dev, &sms) != WSM_OK) return 0;
+    return experts_layout(rows, experts, sms).total;
+}
+
+wsm_status wsm_expert_gemm(const wsm_experts *a, wsm_stream_t stream_) {
+    if (!a) return op_fail(WSM_ERR_INVALID, "the arguments must be non-null");
+    if (a->rows < 0 || a->experts < 1 || a->N < 1)
+        return op_fail(WSM_ERR_INVALID, "rows %d, experts %d, N %d: no negative rows, and an expert and an output at least", a->rows, a->experts, a->N);
+    if (a->experts > kMaxExperts) return op_fail(WSM_ERR_UNSUPPORTED, "%d experts: up to %d are", a->experts, kMaxExperts);
+    if (a->K < 8 || a->K % 8) return op_fail(WSM_ERR_UNSUPPORTED, "unsupported K=%d (need K>=8, K%%8==0)", a->K);
+    if (a->dtype != WSM_DTYPE_BF16 && a->dtype != WSM_DTYPE_FP16)
+        return op_fail(WSM_ERR_UNSUPPORTED, "element type %d: bf16 and fp16 are", a->dtype);
+    if (a->epilogue != WSM_EPI_NONE && a->epilogue != WSM_EPI_SILU_MUL)
+        return op_fail(WSM_ERR_UNSUPPORTED, "epilogue %d: WSM_EPI_NONE and WSM_EPI_SILU_MUL are", a->epilogue);
+    if (a->epilogue == WSM_EPI_SILU_MUL && a->N % 16)
+        return op_fail(WSM_ERR_UNSUPPORTED, "SiLU*mul needs N a multiple of 16 (got %d)", a->N);
+    if (a->rows == 0) return WSM_OK;
+    if (!a->X || !a->W || !a->Y || !a->offsets || !a->workspace)
+        return op_fail(WSM_ERR_INVALID, "X, W, Y, offsets and workspace must be non-null device pointers");
+    if (!aligned_to(a->X, 16) || !aligned_to(a->W, 16) || !aligned_to(a->workspace, 16))
+        return op_fail(WSM_ERR_ALIGN, "X, W and workspace must be 16-byte aligned");
+    if (!aligned_to(a->Y, 2) || !aligned_to(a->offsets, 4) || !aligned_to(a->row_scale, 4))
+        return op_fail(WSM_ERR_ALIGN, "Y, offsets and row_scale must be aligned to their elements");
+    // a stride that no second row, output or expert uses may be anything
+    const long long K = a->K, xs = a->rows > 1 ? a->x_stride : K, wr = a->N > 1 ? a->w_strides[1] : K,
+                    we = a->experts > 1 ? a->w_strides[0] : (long long)a->N * std::max(wr, K);
+    const int y_cols = a->epilogue == WSM_EPI_SILU_MUL ? a->N / 2 : a->N;
+    if (xs % 8 || wr % 8 || we % 8) return op_fail(WSM_ERR_ALIGN, "the strides of X and W must be multiples of 16 bytes");
+    if (xs < K || wr < K || we < (long long)(a->N - 1) * wr + K || (a->rows > 1 && a->y_stride < y_cols))
+        return op_fail(WSM_ERR_INVALID, "rows of X, W or Y overlap: strides %lld, %lld, %lld, %lld", xs, wr, we, a->y_stride);
+    if (xs >= (1ll << 39) || wr >= (1ll << 39) || we >= (1ll << 39)) return op_fail(WSM_ERR_UNSUPPORTED, "a stride is too large");
+    // tiles and their units are counted in 32 bits
+    const long long n_g = ((long long)a->N + kTileN - 1) / kTileN;
+    if (a->rows > (1 << 30) || K > (1 << 30) || n_g * (a->rows / kTileRows + a->experts + 1) >= (1ll << 30))
+        return op_fail(WSM_ERR_UNSUPPORTED, "%d rows by %d outputs of %d terms are too many", a->rows, a->N, a->K);
+    int dev, sms;
+    wsm_status st = device_sms(&dev, &sms);
+    if (st != WSM_OK) return st;
+    const ExLayout l = experts_layout(a->rows, a->experts, sms);
+    if (a->workspace_bytes < l.total)
+        return op_fail(WSM_ERR_NOMEM, "workspace of %zu bytes is smaller than the %zu needed", a->workspace_bytes, l.total);
+
+    const bool bf = a->dtype == WSM_DTYPE_BF16;
+    const CUtensorMapDataType type = bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    ExpertParams p = {};
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)a->N, (cuuint64_t)a->experts};
+        const cuuint64_t strides[2] = {(cuuint64_t)wr * 2, (cuuint64_t)we * 2};
+        const cuuint32_t box[3] = {kBK, kTileN, 1};
+        if ((st = encode_tiled(&p.tmW, type, 3, a->W, dims, strides, box)) != WSM_OK) return st;
+    }
+    const int most = (std::min(a->rows, kTileRows) + 15) / 16 * 16;
+    for (int i = 0; i < kXMaps; ++i) {
+        if ((kTileRows >> i) > most) continue;          // no tile is that high
+        const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)a->rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)xs * 2};
+        const cuuint32_t box[2] = {kBK, (cuuint32_t)(kTileRows >> i)};
+        if ((st = encode_tiled(&p.tmX[i], type, 2, a->X, dims, strides, box)) != WSM_OK) return st;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(a->workspace);
+    p.Y = a->Y;
+    p.offsets = a->offsets;
+    p.row_scale = a->row_scale;
+    p.y_stride = a->y_stride;
+    p.hdr = reinterpret_cast<int *>(ws);
+    p.rec = reinterpret_cast<ExpertRec *>(ws + l.rec);
+    p.tile_cnt = reinterpret_cast<unsigned int *>(ws + l.cnt);
+    p.part = reinterpret_cast<float *>(ws + l.part);
+    p.part_cap = l.part_cap;
+    p.cnt_cap = l.cnt_cap;
+    p.rows = a->rows;
+    p.experts = a->experts;
+    p.N = a->N;
+    p.K = a->K;
+    p.kb = (a->K + kBK - 1) / kBK;
+    p.n_g = (int)n_g;
+    p.silu = a->epilogue == WSM_EPI_SILU_MUL;
+    p.sms = sms;
+    // fp32 accumulators, A and B of one 16-bit type, both K-major, M = 128
+    p.idesc = (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTileN >> 4) << 24);
+    p.stall_ns = take_launch_stall();
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const int plan_threads = (a->experts + 31) / 32 * 32;
+    if ((st = op_launch(&experts_plan_kernel, dim3(1), plan_threads, 0, stream, p)) != WSM_OK) return st;
+    constexpr int kSmem = kStages * kStageBytes + 1024;
+    static volatile bool done[2][kMaxOpDevices] = {};
+    if (bf) {
+        if ((st = op_allow_smem(&experts_kernel<__nv_bfloat16>, kSmem, dev, done[0])) != WSM_OK) return st;
+        return op_launch(&experts_kernel<__nv_bfloat16>, dim3((unsigned)sms), kExThreads, kSmem, stream, p);
+    }
+    if ((st = op_allow_smem(&experts_kernel<__half>, kSmem, dev, done[1])) != WSM_OK) return st;
+    return op_launch(&experts_kernel<__half>, dim3((unsigned)sms), kExThreads, kSmem, stream, p);
+}
+
+}  // extern "C"
