@@ -37,8 +37,11 @@ constexpr int kStages = 4;
 constexpr int kBoxW = kTileN * kBK * 2;
 constexpr int kNarrow = 64;         // up to this many rows a stage holds two K boxes, above one
 constexpr int kNarrowX = kNarrow * kBK * 2;
-constexpr int kXMaps = 5;           // boxes of 256, 128, 64, 32 and 16 rows
-constexpr int kExThreads = 192;
+constexpr int kXMaps = 9;           // boxes of 256, 128, ... 2, 1 rows
+constexpr int kTopBox = 8;          // 256 = 2^8
+constexpr int kUnitRing = 8;        // units announced ahead: one per stage at most, and the end
+constexpr int kEpiSets = 2;
+constexpr int kExThreads = 64 + kEpiSets * 128;
 constexpr uint32_t kExTmemCols = 2 * kTileRows;
 constexpr int kLead = 2;            // a CTA claims its next unit this many stages before its unit ends
 constexpr unsigned long long kExWaitNs = 4000000000ull;
@@ -78,6 +81,11 @@ struct ExpertParams {
 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Rows of X a tile of `rows` loads: a power of two up to 8, then whole groups of 8.
+__device__ __forceinline__ int rows_to_load(int rows) {
+    return rows > 4 ? (rows + 7) & ~7 : rows > 2 ? 4 : rows;
+}
 
 // Tiles along an expert's rows, and the rows of each (cut evenly, a multiple of 16).
 __device__ __forceinline__ int m_tiles_of(int m) { return ceil_div(m, kTileRows); }
@@ -236,6 +244,11 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *
         : "memory");
 }
 
+// z / (1 + e^-z) * up by the hardware's exponential and division, relative error about 2^-20 (below z = -87, where
+// the value is under 2^-119, it is 0): the outputs are rounded to 2^-11 at the finest, and there are as many of
+// these as outputs.
+__device__ __forceinline__ float silu_mul(float z, float up) { return __fdividef(z, 1.f + __expf(-z)) * up; }
+
 // Outputs of one thread: weight row n, rows row0 .. row0 + cnt - 1 of X, sums v.  With SiLU*mul the up value
 // of gate row n comes from the thread of row n + 8 (lane ^ 8); every lane of the warp calls this alike.
 template <typename T>
@@ -253,7 +266,7 @@ __device__ __forceinline__ void emit_rows(const ExpertParams &p, int n, int row0
         float x = v[i];
         if (p.silu) {
             const float up = __shfl_xor_sync(0xffffffffu, x, 8);
-            x = x / (1.f + expf(-x)) * up;
+            x = silu_mul(x, up);
         }
         if (writer) y[i * p.y_stride] = from_f32<T>(x * s[i]);
     }
@@ -263,12 +276,12 @@ template <typename T>
 __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_constant__ ExpertParams p) {
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], accf_bar[2], acce_bar[2], drain_bar;
-    __shared__ int stage_meta[kStages][4];              // {unit, first / last / done, MMA N, K boxes}
-    __shared__ int acc_meta[2];                         // unit, or -1 at the end
+    __shared__ int unit_meta[kUnitRing][4];             // {unit (-1: no more), MMA N, K boxes}, by the producer
+    __shared__ int acc_unit[2];                         // unit of an accumulator (-1: no more), by the MMA thread
     __shared__ int unit0[kMaxExperts];
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
-    __shared__ int last_flag;
+    __shared__ int last_flag[kEpiSets];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     int *const status = g_experts_status;
@@ -296,12 +309,13 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
     const int n_units = p.hdr[kHdrUnits], head = p.hdr[kHdrHead];
+    const uint32_t ring_u = smem_u32(ring);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_normal();
-            int s = 0;
+            int s = 0, slot = 0;
             uint32_t ph = 0;
             long long issued = 0;
             bool aborted = false;
@@ -318,10 +332,17 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
             int u = (int)blockIdx.x;
             while (!aborted && u < n_units) {
                 const Unit t = unit_at(p, unit0, head, u);
-                const bool narrow = t.mrows <= kNarrow;
-                const int step = narrow ? 2 : 1;
+                const int step = t.mrows <= kNarrow ? 2 : 1;
                 // weights with one reader leave L2 first
                 const uint64_t pol_w = p.rec[t.expert].m <= kTileRows ? pol_once : pol_keep;
+                // the rows to load, as box heights: bit i for tmX[i]; rows past them in a narrow tile's MMA width
+                // are what the stage held before, whose sums nobody reads
+                const int load_rows = rows_to_load(t.rows);
+                const uint32_t box_bytes = (uint32_t)(kBoxW + load_rows * kBK * 2);
+                unit_meta[slot][0] = u;
+                unit_meta[slot][1] = t.mrows;
+                unit_meta[slot][2] = t.k1 - t.k0;
+                if (++slot == kUnitRing) slot = 0;
                 int next = n_units;
                 bool claimed = false;
                 for (int k = t.k0; k < t.k1; k += step) {
@@ -330,24 +351,20 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
                         break;
                     }
                     const int boxes = min(step, t.k1 - k);
-                    stage_meta[s][0] = u;
-                    stage_meta[s][1] = (k == t.k0 ? kMetaFirst : 0) | (k + step >= t.k1 ? kMetaLast : 0);
-                    stage_meta[s][2] = t.mrows;
-                    stage_meta[s][3] = boxes;
-                    mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(boxes * (kBoxW + t.mrows * kBK * 2)));
-                    const uint32_t st = smem_u32(ring + (size_t)s * kStageBytes);
+                    mbar_arrive_expect_tx(&full_bar[s], boxes * box_bytes);
+                    const uint32_t st = ring_u + (uint32_t)(s * kStageBytes);
                     for (int b = 0; b < boxes; ++b) {
                         tma_load_3d(st + b * kBoxW, &p.tmW, &full_bar[s], (k + b) * kBK, t.n0, t.expert, pol_w);
                         uint32_t xd = st + step * kBoxW + b * kNarrowX;
-                        int at = t.row0, left = t.mrows;
-                        for (int i = 0; i < kXMaps; ++i) {
+                        int at = t.row0;
+#pragma unroll 1
+                        for (int left = load_rows; left > 0;) {
+                            const int i = __clz(left) - (31 - kTopBox);     // the highest box that fits
                             const int h = kTileRows >> i;
-                            if (left >= h) {
-                                tma_load_2d_at(xd, &p.tmX[i], &full_bar[s], (k + b) * kBK, at, pol_keep);
-                                xd += (uint32_t)(h * kBK * 2);
-                                at += h;
-                                left -= h;
-                            }
+                            tma_load_2d_at(xd, &p.tmX[i], &full_bar[s], (k + b) * kBK, at, pol_keep);
+                            xd += (uint32_t)(h * kBK * 2);
+                            at += h;
+                            left -= h;
                         }
                     }
                     ++issued;
@@ -365,75 +382,95 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
             // every copy has landed before the CTA ends
             drain_issued(full_bar, kStages, issued, kExWaitNs, status);
             if (!aborted && mbar_wait_bounded(&empty_bar[s], ph ^ 1, &abort_flag, kExWaitNs, status, -1, kSiteEmpty)) {
-                stage_meta[s][1] = kMetaDone;
+                unit_meta[slot][0] = -1;
                 mbar_arrive(&full_bar[s]);
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
+        // One thread, and a stage's MMAs take as little as 128 clocks: nothing in the loop over a unit's stages but
+        // the wait, the instructions and the commit.
         if (lane == 0) {
-            int s = 0;
+            int s = 0, slot = 0;
             uint32_t ph = 0, acc_i = 0;
-            int buf = 0;
-            bool any = false;
-            for (;;) {
+            bool ok = true;
+            const uint64_t desc0 = sw128_desc(ring_u);
+            while (ok) {
                 if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag, kExWaitNs, status, -1, kSiteFull)) break;
-                tc_fence_after();
-                const int unit = stage_meta[s][0], flags = stage_meta[s][1], mrows = stage_meta[s][2], boxes = stage_meta[s][3];
-                if (flags & (kMetaFirst | kMetaDone)) {
-                    buf = (int)(acc_i & 1u);
-                    if (!mbar_wait_bounded(&acce_bar[buf], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc)) break;
-                    tc_fence_after();
-                }
-                if (flags & kMetaDone) {
-                    acc_meta[buf] = -1;
+                const int unit = unit_meta[slot][0], mrows = unit_meta[slot][1];
+                int left = unit_meta[slot][2];
+                if (++slot == kUnitRing) slot = 0;
+                const int buf = (int)(acc_i & 1u);
+                if (!mbar_wait_bounded(&acce_bar[buf], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc)) break;
+                if (unit < 0) {
+                    // the end goes to both epilogue sets, the other one's accumulator included
+                    acc_unit[buf] = -1;
                     mbar_arrive(&accf_bar[buf]);
                     mbar_arrive(&accf_bar[buf]);
+                    ++acc_i;
+                    const int other = (int)(acc_i & 1u);
+                    if (!mbar_wait_bounded(&acce_bar[other], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc)) break;
+                    acc_unit[other] = -1;
+                    mbar_arrive(&accf_bar[other]);
+                    mbar_arrive(&accf_bar[other]);
                     break;
                 }
                 const uint32_t idesc = p.idesc | ((uint32_t)(mrows >> 3) << 17);
                 const uint32_t d = tmem_base + (uint32_t)(buf * kTileRows);
-                const uint32_t st = smem_u32(ring + (size_t)s * kStageBytes);
-                const uint32_t x0 = st + (mrows <= kNarrow ? 2 : 1) * kBoxW;
-                for (int b = 0; b < boxes; ++b) {
+                const bool narrow = mrows <= kNarrow;
+                const uint64_t x_off = (uint64_t)(((narrow ? 2 : 1) * kBoxW) >> 4);
+                uint32_t add = 0u;
+                tc_fence_after();
+                for (;;) {
+                    const uint64_t a = desc0 + (uint64_t)(s * (kStageBytes >> 4)), b = a + x_off;
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)
-                        tc_mma(d, sw128_desc(st + b * kBoxW + 32u * k), sw128_desc(x0 + b * kNarrowX + 32u * k), idesc,
-                               ((flags & kMetaFirst) && b == 0 && k == 0) ? 0u : 1u);
+                    for (int k = 0; k < kBK / 16; ++k) {        // 16 K elements are 32 bytes of a swizzle row
+                        tc_mma(d, a + 2u * k, b + 2u * k, idesc, add);
+                        add = 1u;
+                    }
+                    if (narrow && left > 1) {
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k)
+                            tc_mma(d, a + (kBoxW >> 4) + 2u * k, b + (kNarrowX >> 4) + 2u * k, idesc, 1u);
+                    }
+                    tc_commit(&empty_bar[s]);
+                    left -= narrow ? 2 : 1;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                    if (left <= 0) break;
+                    if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag, kExWaitNs, status, -1, kSiteFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                 }
-                any = true;
-                tc_commit(&empty_bar[s]);
-                if (flags & kMetaLast) {
-                    acc_meta[buf] = unit;
-                    mbar_arrive(&accf_bar[buf]);
-                    tc_commit(&accf_bar[buf]);
-                    ++acc_i;
-                }
-                if (++s == kStages) {
-                    s = 0;
-                    ph ^= 1;
-                }
+                if (!ok) break;
+                acc_unit[buf] = unit;
+                mbar_arrive(&accf_bar[buf]);
+                tc_commit(&accf_bar[buf]);
+                ++acc_i;
             }
-            if (any) {
-                // all MMAs are complete before tensor memory is released
-                tc_commit(&drain_bar);
-                volatile int never = 0;
-                mbar_wait_bounded(&drain_bar, 0, &never, kExWaitNs, status, -1, kSiteDrain);
-            }
+            // all MMAs are complete before tensor memory is released
+            tc_commit(&drain_bar);
+            volatile int never = 0;
+            mbar_wait_bounded(&drain_bar, 0, &never, kExWaitNs, status, -1, kSiteDrain);
         }
     } else {
         // ------------------------------------------------------------ epilogue
+        // Two sets of four warps, one for each accumulator.
+        const int set = (warp - 2) >> 2;
         const int q = warp & 3;                         // TMEM lane quadrant this warp may read
         const int row = q * 32 + lane;                  // weight row within the tile
-        const bool leader = threadIdx.x == 64;
+        const bool leader = (threadIdx.x - 64) == (unsigned)(set * 128);
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(set * kTileRows);
         for (uint32_t i = 0;; ++i) {
-            const int buf = (int)(i & 1u);
-            const bool ab = !mbar_wait_bounded(&accf_bar[buf], (i >> 1) & 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc);
-            const int u = ab ? -1 : acc_meta[buf];
-            if (vote_or(u < 0, 1, 128)) break;          // the four warps stop together
+            const bool ab = !mbar_wait_bounded(&accf_bar[set], i & 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc);
+            const int u = ab ? -1 : acc_unit[set];
+            if (vote_or(u < 0, 1 + set, 128)) break;    // the four warps stop together
             tc_fence_after();
             const Unit t = unit_at(p, unit0, head, u);
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTileRows);
             float *part = p.part + ((size_t)t.part + (size_t)t.j * (t.mrows / 16)) * (16 * kTileN) + row;
 #pragma unroll 1
             for (int c = 0; c < t.rows; c += 16) {
@@ -453,13 +490,13 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acce_bar[buf]);
+            if (lane == 0) mbar_arrive(&acce_bar[set]);
             if (t.nu == 1) continue;
             // the tile's last unit to arrive adds all partials, in K order
-            named_bar_sync(2, 128);
-            if (leader) last_flag = atom_add_acqrel_gpu(&p.tile_cnt[t.split], 1u) == (unsigned int)(t.nu - 1) ? 1 : 0;
-            named_bar_sync(2, 128);
-            if (!last_flag) continue;
+            named_bar_sync(3 + set, 128);
+            if (leader) last_flag[set] = atom_add_acqrel_gpu(&p.tile_cnt[t.split], 1u) == (unsigned int)(t.nu - 1) ? 1 : 0;
+            named_bar_sync(3 + set, 128);
+            if (!last_flag[set]) continue;
             const float *from = p.part + (size_t)t.part * (16 * kTileN) + row;
             const size_t step = (size_t)(t.mrows / 16) * (16 * kTileN);
 #pragma unroll 1
