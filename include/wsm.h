@@ -642,14 +642,17 @@ typedef struct {
     const int *lengths;      /* [batch] */
     long long q_strides[2], o_strides[2];
     long long table_stride;
-    void *workspace;         /* device, 16-byte aligned, wsm_paged_attention_workspace_bytes */
+    void *workspace;         /* device, 16-byte aligned, wsm_paged_attention_workspace; NULL when it needs none */
     size_t workspace_bytes;
     int batch, heads, max_pages;
     int window;              /* 0: no window */
     int dtype;               /* of Q and O: WSM_DTYPE_BF16 or _FP16; a 16-bit cache has the same */
     float scale;
 } wsm_attention;
-size_t wsm_paged_attention_workspace_bytes(int batch, int head_dim);  /* current device; 0 on error */
+/* Scratch for sequences of up to max_tokens (max_pages * page_size) tokens on the current device: *bytes, 0
+ * where no sequence can be long enough to be cut. */
+wsm_status wsm_paged_attention_workspace(int batch, int head_dim, int cache_dtype, long long max_tokens, int window,
+                                         size_t *bytes);
 wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *args, wsm_stream_t stream);
 
 /* Products grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of X belong

@@ -60,7 +60,7 @@ def rows(**kw):
 
 
 def attention(**kw):
-    a = dict(Q=P, O=P, lse=0, table=P, lengths=P, qs=(256, 64), os=(256, 64), ts=8, ws=P, wsb=1 << 30, batch=2, heads=4, pages=8,
+    a = dict(Q=P, O=P, lse=0, table=P, lengths=P, qs=(256, 64), os=(256, 64), ts=8, ws=P, wsb=1 << 30, batch=2, heads=4, pages=64,
              window=0, dtype=0, scale=0.125)
     a.update(kw)
     return operators._ATTENTION.pack(a["Q"], a["O"], a["lse"], a["table"], a["lengths"], *a["qs"], *a["os"], a["ts"], a["ws"],
@@ -132,10 +132,17 @@ def test_attention_dims_null_and_zero():
     for dim in (16, 32, 80, 112, 512):
         c = cache(dim=dim, ks=(32 * dim, 2 * dim, dim), vs=(32 * dim, 2 * dim, dim))
         assert L.wsm_paged_attention(c, attention(), None) == UNSUPPORTED
-        assert L.wsm_paged_attention_workspace_bytes(1, dim) == 0
+        assert L.wsm_paged_attention_workspace(1, dim, 0, 1000, 0, ctypes.byref(ctypes.c_size_t())) == UNSUPPORTED
     assert L.wsm_paged_attention(cache(), None, None) == INVALID
     assert L.wsm_paged_attention(cache(), attention(batch=0, Q=0, O=0, lengths=0, table=0, ws=0), None) == wsm.WSM_OK
-    assert L.wsm_paged_attention_workspace_bytes(4097, 64) == 0 and L.wsm_paged_attention_workspace_bytes(-1, 64) == 0
+    n = ctypes.c_size_t(7)
+    assert L.wsm_paged_attention_workspace(4097, 64, 0, 1000, 0, ctypes.byref(n)) == UNSUPPORTED
+    for bad in ((-1, 64, 0, 1000, 0), (1, 64, 0, -1, 0), (1, 64, 0, 1000, -1)):
+        assert L.wsm_paged_attention_workspace(*bad, ctypes.byref(n)) == INVALID
+    assert L.wsm_paged_attention_workspace(1, 64, 0, 1000, 0, None) == INVALID
+    # sequences that are never cut need none
+    assert L.wsm_paged_attention_workspace(9, 64, 0, 128, 0, ctypes.byref(n)) == wsm.WSM_OK and n.value == 0
+    assert L.wsm_paged_attention_workspace(9, 64, 0, 10 ** 6, 100, ctypes.byref(n)) == wsm.WSM_OK and n.value == 0
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -187,10 +194,10 @@ def test_python_calls_refuse_what_is_no_cuda_tensor():
                  lambda: wsm.token_logprobs(q[0])):
         with pytest.raises(ValueError, match="CUDA"):
             call()
-    with pytest.raises(TypeError):
-        wsm.token_logprobs([[1.0]])
-    with pytest.raises(TypeError):
-        wsm.paged_cache_append(None, q, c, c, i)
+    for call in (lambda: wsm.token_logprobs([[1.0]]), lambda: wsm.paged_cache_append(None, q, c, c, i),
+                 lambda: wsm.paged_attention(None, c, c, i, i), lambda: wsm.expert_gemm(None, q, i)):
+        with pytest.raises(TypeError, match="torch tensor"):
+            call()
 
 
 # ------------------------------------------------------------------ the oracle itself

@@ -50,7 +50,7 @@ HEADER_SYMBOLS = (
     "wsm_chain_trace",
     "wsm_chain_destroy",
     "gemm_chain", "wsm_chain_validate", "wsm_last_error", "wsm_abi_version",
-    "wsm_paged_cache_append", "wsm_paged_attention_workspace_bytes", "wsm_paged_attention",
+    "wsm_paged_cache_append", "wsm_paged_attention_workspace", "wsm_paged_attention",
     "wsm_expert_gemm_workspace_bytes", "wsm_expert_gemm", "wsm_token_logprobs", "wsm_operator_status",
 )
 
@@ -166,8 +166,8 @@ def lib() -> ctypes.CDLL:
         L.wsm_paged_cache_append.restype = st
         L.wsm_paged_attention.argtypes = [vp, vp, vp]
         L.wsm_paged_attention.restype = st
-        L.wsm_paged_attention_workspace_bytes.argtypes = [i, i]
-        L.wsm_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.wsm_paged_attention_workspace.argtypes = [i, i, i, ctypes.c_longlong, i, ctypes.POINTER(ctypes.c_size_t)]
+        L.wsm_paged_attention_workspace.restype = st
         L.wsm_expert_gemm.argtypes = [vp, vp]
         L.wsm_expert_gemm.restype = st
         L.wsm_expert_gemm_workspace_bytes.argtypes = [i, i]

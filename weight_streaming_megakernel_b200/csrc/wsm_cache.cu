@@ -121,8 +121,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
 constexpr int kGroup = 16;          // tokens a warp takes at a time (the MMA's k)
 constexpr int kMaxBatch = 4096;     // sequences per call: their group prefix sums sit in shared memory
-constexpr int kMinGroups = 4;       // least groups per warp ...
-constexpr int kSnapGroups = 8;      // ... and items of up to this many groups (128 tokens) are never cut
+constexpr int kMinShare = 4;        // least length of a warp's range: no more than the shortest item's
+constexpr int kSnapGroups = 8;      // items of up to this many groups (128 tokens) are never cut
+// What beginning and ending an item costs a warp, in groups: counted when the work is dealt out, so that a warp
+// with many short sequences does not finish last.
+constexpr int kItemCost = 3;
 
 struct AttnParams {
     const uint8_t *Q;
@@ -140,9 +143,11 @@ struct AttnParams {
     float sl2;                      // scale * k_scale * log2(e)
     float v_scale;
     int batch, heads, kv_heads, group, q_tiles;    // group = heads / kv_heads
-    int page_size, max_tokens, window;
+    int page_size, page_shift, max_tokens, window; // page_shift: log2 of page_size, or -1
+    int kv_alike;                   // K and V have the same strides
+    int far;                        // some row lies 2^32 or more 16-byte units into its cache
     int workers;
-    int rows_per_cta;               // join: rows of an item one block takes
+    int rows_per_cta, join_split;   // join: rows of an item one block takes, and the warps for each
 };
 
 // The tokens a sequence attends to, [first, len), and its groups: kGroup-aligned from first down.
@@ -158,33 +163,50 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
     return s;
 }
 
-// Groups per worker.
-__device__ __forceinline__ long long share_of(long long total, int workers) {
-    const long long per = (total + workers - 1) / workers;
-    return per < kMinGroups ? kMinGroups : per;
+// The work in a line: sequence b's items follow one another, each kItemCost + groups long, so b begins at
+// (prefix[b] + kItemCost * b) * hq with prefix the groups before b.  (At most 2^31 - 1 in all: checked by the host.)
+__device__ __forceinline__ int line_of(const int *prefix, int hq, int b) { return (prefix[b] + kItemCost * b) * hq; }
+
+// Length of a warp's range.
+__device__ __forceinline__ int share_of(int total, int workers) {
+    const int per = (total + workers - 1) / workers;
+    return per < kMinShare ? kMinShare : per;
 }
 
-// The sequence that flattened group `pos` belongs to (pos < total): prefix[b] * hq <= pos < prefix[b + 1] * hq.
-__device__ __forceinline__ int seq_of(const int *prefix, int batch, int hq, long long pos) {
+// The sequence at place `pos` of the line.
+__device__ __forceinline__ int seq_of(const int *prefix, int batch, int hq, int pos) {
     int lo = 0, hi = batch - 1;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)prefix[mid + 1] * hq > pos) hi = mid;
+        if (line_of(prefix, hq, mid + 1) > pos) hi = mid;
         else lo = mid + 1;
     }
     return lo;
 }
 
-// A worker's boundary: w * per, moved down to the start of its item where that item is short.
-__device__ __forceinline__ long long boundary_of(const int *prefix, int batch, int hq, long long total, long long per,
-                                                 int w) {
-    const long long pos = w * per;
-    if (pos >= total) return total;
-    const int b = seq_of(prefix, batch, hq, pos);
-    const int n = prefix[b + 1] - prefix[b];
-    if (n > kSnapGroups) return pos;
-    const long long at = (long long)prefix[b] * hq;
-    return at + (pos - at) / n * n;
+// Where range w begins: sequence, item and group.  A range that would begin within an item's fixed cost, or
+// within a short item, begins with the item.
+struct Place {
+    int b, item, g;
+};
+__device__ __forceinline__ Place place_of(const int *prefix, int batch, int hq, int total, int per, int w) {
+    Place r;
+    const long long pos = (long long)w * per;
+    if (pos >= total) {
+        r.b = batch;
+        r.item = r.g = 0;
+        return r;
+    }
+    r.b = seq_of(prefix, batch, hq, (int)pos);
+    const int n = prefix[r.b + 1] - prefix[r.b], off = (int)pos - line_of(prefix, hq, r.b);
+    r.item = off / (n + kItemCost);
+    r.g = n <= kSnapGroups ? 0 : max(0, off - r.item * (n + kItemCost) - kItemCost);
+    return r;
+}
+// Groups before a place.
+__device__ __forceinline__ int groups_before(const int *prefix, int hq, const Place &r, int batch) {
+    if (r.b >= batch) return prefix[batch] * hq;
+    return prefix[r.b] * hq + r.item * (prefix[r.b + 1] - prefix[r.b]) + r.g;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -222,10 +244,12 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 values (low 16 bits) as fp16: exact.
-__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 values as fp16, two to a register: exact.
+__device__ __forceinline__ void e4m3x4_half2(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
 
 // Block geometry of one instantiation: as many warps and ring stages as registers and shared memory hold.
@@ -233,7 +257,8 @@ __device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t v) {
 template <int D, int ESZ> struct AttnGeo {
     static constexpr int kRow = D * ESZ + 16;           // padded: 8 rows of one 16-byte column in 8 bank groups
     static constexpr int kStage = 2 * kGroup * kRow;
-    static constexpr int kWarps = D >= 256 ? 4 : 8;
+    // 4 KB groups want more warps: a warp's own latency per group, about 1500 clocks, bounds 8 of them
+    static constexpr int kWarps = D >= 256 ? 4 : D * ESZ <= 128 ? 12 : 8;
     static constexpr int kFit = 206 * 1024 / (kWarps * kStage);
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kRing = kWarps * kStages * kStage;
@@ -283,105 +308,143 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             carry += s;
         }
         if (b < p.batch) prefix[b + 1] = before + v;
+        if (b == 0) prefix[0] = 0;
         __syncthreads();
     }
-    if (threadIdx.x == 0) prefix[0] = 0;
-    __syncthreads();
-    if (blockIdx.x == 0)
+    if (p.prefix && blockIdx.x == 0)
         for (int b = threadIdx.x; b <= p.batch; b += NW * 32) p.prefix[b] = prefix[b];
 
+    // ---- this warp's range; neighbouring ranges lie on different SMs, so a short call's few spread over the GPU
+    const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
+    const int total = line_of(prefix, hq, p.batch);
+    const int per = share_of(total, p.workers);
+
     // ---- sequences without a token to attend to: zeros, and the empty sum's logarithm
-    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    for (int b = worker; b < p.batch; b += p.workers) {
         if (prefix[b + 1] != prefix[b]) continue;
-        for (int i = threadIdx.x; i < p.heads * (D / 2); i += NW * 32) {
-            const int h = i / (D / 2), d = (i - h * (D / 2)) * 2;
-            *reinterpret_cast<uint32_t *>(reinterpret_cast<T *>(p.O) + b * p.o_row + h * p.o_head + d) = 0u;
+        for (int h = 0; h < p.heads; ++h) {
+            T *out = reinterpret_cast<T *>(p.O) + b * p.o_row + h * p.o_head;
+            for (int d = lane * 8; d < D; d += 256) *reinterpret_cast<uint4 *>(out + d) = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse && lane == 0) p.lse[(long long)b * p.heads + h] = -INFINITY;
         }
-        if (p.lse)
-            for (int h = threadIdx.x; h < p.heads; h += NW * 32) p.lse[(long long)b * p.heads + h] = -INFINITY;
     }
 
-    // ---- this warp's range
-    const long long total = (long long)prefix[p.batch] * hq;
-    const long long per = share_of(total, p.workers);
-    // neighbouring ranges on different SMs: a range's length is the same for all, but a short call's few
-    // ranges then spread over the GPU
-    const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
-    const long long begin = boundary_of(prefix, p.batch, hq, total, per, worker);
-    const long long end = boundary_of(prefix, p.batch, hq, total, per, worker + 1);
-    if (begin >= end) return;
-    const int n_groups = (int)(end - begin);
+    // (odd lanes work out where the next range begins, even ones where this does)
+    Place first = place_of(prefix, p.batch, hq, total, per, worker + (lane & 1));
+    const int mine = groups_before(prefix, hq, first, p.batch);
+    const int n_groups = __shfl_sync(0xffffffffu, mine, 1) - __shfl_sync(0xffffffffu, mine, 0);
+    if (n_groups <= 0) return;
+    first.b = __shfl_sync(0xffffffffu, first.b, 0);
+    first.item = __shfl_sync(0xffffffffu, first.item, 0);
+    first.g = __shfl_sync(0xffffffffu, first.g, 0);
 
     uint8_t *ring = smem + warp * (NS * Geo::kStage);
     const uint32_t ring_u = smem_u32(ring);
 
-    // ---- the load side: where the next group to fetch lies
-    int lb = seq_of(prefix, p.batch, hq, begin);
+    // ---- the load side: where the next group to look up lies
+    int lb = first.b, litem = first.item, lg = first.g;
+    while (prefix[lb + 1] == prefix[lb]) {              // (the range holds groups, so a sequence that has some follows)
+        ++lb;
+        litem = lg = 0;
+    }
+    const Place start = {lb, litem, lg};
     Span ls = span_of(p, p.lengths[lb]);
-    int litem = (int)((begin - (long long)prefix[lb] * hq) / ls.groups);
-    int lg = (int)(begin - (long long)prefix[lb] * hq - (long long)litem * ls.groups);
-    // the page of this lane's token (lane & 15) of the next group to load, fetched one group ahead
-    int next_page = -1, next_off = 0;
-    bool next_in = false;
-    auto look_up = [&]() {
-        const int tok = ls.base + lg * kGroup + (lane & 15);
-        next_in = tok >= ls.first && tok < ls.len;
-        if (next_in) {
-            const int pi = tok / p.page_size;
-            next_off = tok - pi * p.page_size;
-            next_page = p.table[lb * p.table_stride + pi];
-        }
+    const int start_groups = ls.groups;
+    int next_len = lb + 1 < p.batch ? p.lengths[lb + 1] : 0;    // fetched a sequence ahead
+    // Two groups at a time, looked up two groups ahead: lanes 0-15 hold the page of the even group's tokens, lanes
+    // 16-31 that of the odd one's.
+    struct Pages {
+        int page, off, seq, head;
+        bool in;
     };
-    look_up();
-    auto load_group = [&](int stage) {
-        const bool ok = next_in && (unsigned long long)(long long)next_page < (unsigned long long)p.num_pages;
-        if (next_in && !ok && lane < 16) record_op_error(g_cache_status, kCodeInvalid, lb, kSitePage);
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-        if (lane == 0) stage_mask[warp][stage] = mask;
-        const int h = litem / p.q_tiles;
-        const long long ko = ok ? next_page * p.k_page + next_off * p.k_tok + h * p.k_head : 0;
-        const long long vo = ok ? next_page * p.v_page + next_off * p.v_tok + h * p.v_head : 0;
-        const uint32_t st = ring_u + (uint32_t)(stage * Geo::kStage);
-        // chunk i of lane: consecutive lanes take consecutive 16-byte chunks of a row
+    int looked = 0;                                     // groups looked up
+    auto look_up = [&]() {
+        Pages r;
+        r.page = -1;
+        r.off = r.seq = r.head = 0;
+        r.in = false;
 #pragma unroll
-        for (int i = 0; i < kGroup * CH / 32; ++i) {
-            const int idx = i * 32 + lane;
-            const int row = idx / CH, ch = idx % CH;
-            const uint32_t bytes = ((mask >> row) & 1u) ? 16u : 0u;     // rows that are not there read as zeros
-            const long long ro = __shfl_sync(0xffffffffu, ko, row);
-            cp_async16(st + (uint32_t)(row * Geo::kRow + ch * 16), p.K + ro * ESZ + ch * 16, bytes);
+        for (int half = 0; half < 2; ++half) {
+            if (looked < n_groups) {
+                if ((lane >> 4) == half) {
+                    const int tok = ls.base + lg * kGroup + (lane & 15);
+                    r.in = tok >= ls.first && tok < ls.len;
+                    r.seq = lb;
+                    r.head = p.q_tiles == 1 ? litem : litem / p.q_tiles;
+                    if (r.in) {
+                        const int pi = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
+                        r.off = tok - pi * p.page_size;
+                        r.page = p.table[lb * p.table_stride + pi];
+                    }
+                }
+                ++looked;
+                // the next group, over sequences without any
+                if (++lg == ls.groups) {
+                    lg = 0;
+                    if (++litem == hq && looked < n_groups) {
+                        litem = 0;
+                        ++lb;
+                        int len = next_len;
+                        while (prefix[lb + 1] == prefix[lb]) len = p.lengths[++lb];
+                        ls = span_of(p, len);
+                        next_len = lb + 1 < p.batch ? p.lengths[lb + 1] : 0;
+                    }
+                }
+            }
         }
+        return r;
+    };
+    Pages ahead = look_up();
+    // of the pair being loaded: which tokens are there, and where their rows lie, in 16-byte units
+    uint32_t there = 0u, k_lo = 0u, k_hi = 0u, v_lo = 0u, v_hi = 0u;
+    auto load_group = [&](int k, int stage) {
+        if ((k & 1) == 0) {
+            const Pages now = ahead;
+            const bool ok = now.in && (unsigned)now.page < (unsigned)p.num_pages;
+            if (now.in && !ok) record_op_error(g_cache_status, kCodeInvalid, now.seq, kSitePage);
+            there = __ballot_sync(0xffffffffu, ok);
+            const unsigned long long ko = ok ? (now.page * p.k_page + now.off * p.k_tok + now.head * p.k_head) * ESZ / 16 : 0;
+            k_lo = (uint32_t)ko;
+            k_hi = (uint32_t)(ko >> 32);
+            if (!p.kv_alike) {
+                const unsigned long long vo = ok ? (now.page * p.v_page + now.off * p.v_tok + now.head * p.v_head) * ESZ / 16 : 0;
+                v_lo = (uint32_t)vo;
+                v_hi = (uint32_t)(vo >> 32);
+            }
+            ahead = look_up();
+        }
+        const int half = (k & 1) * 16;
+        const uint32_t mask = (there >> half) & 0xffffu;
+        if (lane == 0) stage_mask[warp][stage] = mask;
+        const uint32_t st = ring_u + (uint32_t)(stage * Geo::kStage);
+        // consecutive lanes take consecutive 16-byte chunks of a row; rows that are not there read as zeros
 #pragma unroll
         for (int i = 0; i < kGroup * CH / 32; ++i) {
             const int idx = i * 32 + lane;
             const int row = idx / CH, ch = idx % CH;
             const uint32_t bytes = ((mask >> row) & 1u) ? 16u : 0u;
-            const long long ro = __shfl_sync(0xffffffffu, vo, row);
-            cp_async16(st + (uint32_t)(kGroup * Geo::kRow + row * Geo::kRow + ch * 16), p.V + ro * ESZ + ch * 16, bytes);
-        }
-        // step to the next group, over sequences without any
-        if (++lg == ls.groups) {
-            lg = 0;
-            if (++litem == hq) {
-                litem = 0;
-                do {
-                    ++lb;
-                } while (lb < p.batch && prefix[lb + 1] == prefix[lb]);
-                if (lb < p.batch) ls = span_of(p, p.lengths[lb]);
+            const uint32_t dst = st + (uint32_t)(row * Geo::kRow + ch * 16);
+            unsigned long long rk = __shfl_sync(0xffffffffu, k_lo, half + row);
+            if (p.far) rk |= (unsigned long long)__shfl_sync(0xffffffffu, k_hi, half + row) << 32;
+            unsigned long long rv = rk;
+            if (!p.kv_alike) {
+                rv = __shfl_sync(0xffffffffu, v_lo, half + row);
+                if (p.far) rv |= (unsigned long long)__shfl_sync(0xffffffffu, v_hi, half + row) << 32;
             }
+            cp_async16(dst, p.K + rk * 16 + ch * 16, bytes);
+            cp_async16(dst + (uint32_t)(kGroup * Geo::kRow), p.V + rv * 16 + ch * 16, bytes);
         }
     };
 
     // ---- the compute side
-    int cb = lb;
-    int cgroups = ls.groups, citem = litem, cg = lg;
-    long long seg_begin = begin;                        // where the current item's part of this range begins
+    int cb = start.b, cgroups = start_groups, citem = start.item, cg = start.g;
+    int seg_begin = 0;                                  // where the current item's part of this range begins
     const int g = lane >> 2, t = lane & 3;
     uint32_t qa[KS][4];
     float o[2 * KS][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, f0 = 0.f, f1 = 0.f;
     auto begin_item = [&]() {
-        const int h = citem / p.q_tiles, qt = citem - h * p.q_tiles;
+        const int h = p.q_tiles == 1 ? citem : citem / p.q_tiles, qt = citem - h * p.q_tiles;
         const int rows = min(16, p.group - qt * 16);
         const T *q = reinterpret_cast<const T *>(p.Q) + cb * p.q_row + (long long)(h * p.group + qt * 16) * p.q_head;
 #pragma unroll
@@ -429,10 +492,16 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         for (int i = 0; i < 2 * KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         m0 = m1 = -INFINITY;
         l0 = l1 = 0.f;
+        // the following item's queries into L1 meanwhile (the next heads of this sequence, or the next sequence's)
+        const T *qn = citem + 1 < hq ? q + (long long)rows * p.q_head
+                                     : reinterpret_cast<const T *>(p.Q) + min(cb + 1, p.batch - 1) * p.q_row;
+        const int ahead_rows = min(16, citem + 1 < hq ? p.heads - (h * p.group + qt * 16 + rows) : p.group);
+        for (int i = lane; i < ahead_rows * (D / 64); i += 32)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(qn + (i / (D / 64)) * p.q_head + (i % (D / 64)) * 64));
     };
     // the item's last group in this range is done: outputs when the range holds all of it, else a partial
-    auto finish_item = [&](long long seg_end) {
-        const int h = citem / p.q_tiles, qt = citem - h * p.q_tiles;
+    auto finish_item = [&](int seg_end) {
+        const int h = p.q_tiles == 1 ? citem : citem / p.q_tiles, qt = citem - h * p.q_tiles;
         const int rows = min(16, p.group - qt * 16);
 #pragma unroll
         for (int x = 1; x < 4; x <<= 1) {
@@ -479,7 +548,10 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             }
             return;
         }
-        const int slot = worker * 2 + (seg_begin == begin ? 0 : 1);
+        // first slot: the range begins in this item; else the item begins in the range (a range holds parts of one
+        // item of either kind at most)
+        const int slot = worker * 2 +
+                         ((long long)worker * per >= line_of(prefix, hq, cb) + citem * (cgroups + kItemCost) ? 0 : 1);
         float *po = p.part_o + (size_t)slot * 16 * D;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -505,8 +577,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
 
     int loaded = 0;
     for (; loaded < NS - 1 && loaded < n_groups; ++loaded) {
-        load_group(loaded);
-        if (loaded + 1 < n_groups) look_up();
+        load_group(loaded, loaded);
         cp_async_commit();
     }
     for (int i = loaded; i < NS - 1; ++i) cp_async_commit();   // empty groups keep the wait's count
@@ -522,8 +593,8 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         __syncwarp();                                   // the group is in shared memory, and its mask; the stage
                                                         // refilled next has been read by every lane
         if (loaded < n_groups) {
-            load_group(fill);
-            if (++loaded < n_groups) look_up();
+            load_group(loaded, fill);
+            ++loaded;
         }
         cp_async_commit();
         if (++fill == NS) fill = 0;
@@ -538,10 +609,12 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             uint32_t b[4];
             ldsm4(st + k_lane + (uint32_t)(ks * 16 * ESZ), b);
             if constexpr (kE4m3) {
-                mma16816<M>(s[0][0], qa[ks], e4m3x2_half2(b[0]), e4m3x2_half2(b[0] >> 16));
-                mma16816<M>(s[0][1], qa[ks], e4m3x2_half2(b[1]), e4m3x2_half2(b[1] >> 16));
-                mma16816<M>(s[1][0], qa[ks + 1], e4m3x2_half2(b[2]), e4m3x2_half2(b[2] >> 16));
-                mma16816<M>(s[1][1], qa[ks + 1], e4m3x2_half2(b[3]), e4m3x2_half2(b[3] >> 16));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t lo, hi;
+                    e4m3x4_half2(b[c], lo, hi);
+                    mma16816<M>(s[c >> 1][c & 1], qa[ks + (c >> 1)], lo, hi);
+                }
             } else {
                 mma16816<M>(s[ks & 1][0], qa[ks], b[0], b[1]);
                 mma16816<M>(s[ks & 1][1], qa[ks], b[2], b[3]);
@@ -552,9 +625,16 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const bool in = (mask >> (nt * 8 + 2 * t + j)) & 1u;
-                x0[nt * 2 + j] = in ? (s[0][nt][j] + s[1][nt][j]) * f0 : -INFINITY;
-                x1[nt * 2 + j] = in ? (s[0][nt][2 + j] + s[1][nt][2 + j]) * f1 : -INFINITY;
+                x0[nt * 2 + j] = (s[0][nt][j] + s[1][nt][j]) * f0;
+                x1[nt * 2 + j] = (s[0][nt][2 + j] + s[1][nt][2 + j]) * f1;
+            }
+        }
+        if (mask != 0xffffu) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = (mask >> ((j >> 1) * 8 + 2 * t + (j & 1))) & 1u;
+                x0[j] = in ? x0[j] : -INFINITY;
+                x1[j] = in ? x1[j] : -INFINITY;
             }
         }
         float n0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3]));
@@ -568,7 +648,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             n0 = fmaxf(n0, m0);
             n1 = fmaxf(n1, m1);
             // (a maximum still at -infinity has summed nothing yet)
-            const float a0 = n0 == m0 ? 1.f : exp2f(m0 - n0), a1 = n1 == m1 ? 1.f : exp2f(m1 - n1);
+            const float a0 = n0 == m0 ? 1.f : ex2(m0 - n0), a1 = n1 == m1 ? 1.f : ex2(m1 - n1);
             m0 = n0;
             m1 = n1;
             l0 *= a0;
@@ -584,8 +664,8 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x0[j] = exp2f(x0[j] - z0);
-            x1[j] = exp2f(x1[j] - z1);
+            x0[j] = ex2(x0[j] - z0);
+            x1[j] = ex2(x1[j] - z1);
             l0 += x0[j];
             l1 += x1[j];
         }
@@ -600,9 +680,11 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
                 // a register holds two tokens of two columns: even column to one tile, odd to the next
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint32_t lo = __byte_perm(b[2 * c], 0, 0x3120), hi = __byte_perm(b[2 * c + 1], 0, 0x3120);
-                    mma16816<M>(o[2 * (ks + c)], pa, e4m3x2_half2(lo), e4m3x2_half2(hi));
-                    mma16816<M>(o[2 * (ks + c) + 1], pa, e4m3x2_half2(lo >> 16), e4m3x2_half2(hi >> 16));
+                    uint32_t even0, odd0, even1, odd1;
+                    e4m3x4_half2(__byte_perm(b[2 * c], 0, 0x3120), even0, odd0);
+                    e4m3x4_half2(__byte_perm(b[2 * c + 1], 0, 0x3120), even1, odd1);
+                    mma16816<M>(o[2 * (ks + c)], pa, even0, even1);
+                    mma16816<M>(o[2 * (ks + c) + 1], pa, odd0, odd1);
                 }
             } else {
                 mma16816<M>(o[2 * ks], pa, b[0], b[1]);
@@ -612,9 +694,9 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         // the item or the range ends here
         ++cg;
         if (cg == cgroups || i + 1 == n_groups) {
-            finish_item(begin + i + 1);
+            finish_item(i + 1);
             if (i + 1 < n_groups) {
-                seg_begin = begin + i + 1;
+                seg_begin = i + 1;
                 cg = 0;
                 if (++citem == hq) {
                     citem = 0;
@@ -630,87 +712,115 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
     cp_async_wait<0>();
 }
 
-// Join the partials of the items that were cut: block (item, rows).  Warps take every NW-th partial of a row,
-// in range order, and their sums are added in warp order: the same result every time.
-constexpr int kJoinWarps = 8;
+// Join the partials of the items that were cut: block (item, rows).  Each row's partials are dealt to as many
+// warps as there are for it (p.join_split), which take every join_split-th in range order, kJoinUnroll at a time;
+// the warps' sums are added in warp order: the same result every time.
+constexpr int kJoinWarps = 16;
+constexpr int kJoinUnroll = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float4 sum[kJoinWarps][D / 4];
     __shared__ float2 ml[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait();
-    pdl_launch_dependents();
     const int hq = p.kv_heads * p.q_tiles;
     const int b = (int)blockIdx.x / hq, item = (int)blockIdx.x - b * hq;
-    const int *prefix = p.prefix;
-    const long long first = prefix[b];
-    const int n = prefix[b + 1] - (int)first;
-    if (n <= kSnapGroups) return;                       // never cut
-    const long long per = share_of((long long)prefix[p.batch] * hq, p.workers);
-    const long long at = first * hq + (long long)item * n;
-    const int w0 = (int)(at / per), w1 = (int)((at + n - 1) / per);
-    if (w0 == w1) return;                               // one range holds it
-    const int h = item / p.q_tiles, qt = item - h * p.q_tiles;
+    const int h = p.q_tiles == 1 ? item : item / p.q_tiles, qt = item - h * p.q_tiles;
     const int rows = min(16, p.group - qt * 16);
-    // its first range begins before the item (second slot) unless the two begin together
-    const int slot0 = w0 * 2 + (at == w0 * per ? 0 : 1);
-    const int r_end = min(rows, ((int)blockIdx.y + 1) * p.rows_per_cta);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int *prefix = p.prefix;
+    const int n = prefix[b + 1] - prefix[b], at = line_of(prefix, hq, b) + item * (n + kItemCost);
+    const int per = share_of(line_of(prefix, hq, p.batch), p.workers);
+    if (n <= kSnapGroups) return;                       // never cut
+    // group g lies kItemCost + g past the item's place in the line; the ranges of the first and the last one
+    const int w0 = (at + kItemCost) / per, w1 = (at + kItemCost + n - 1) / per;
+    if (w0 == w1) return;                               // one range holds it
+    const int slot0 = w0 * 2 + ((long long)w0 * per >= at ? 0 : 1);
+    const int split = p.join_split, wr = warp / split, ws = warp - wr * split;
+    const int r = (int)blockIdx.y * p.rows_per_cta + wr;
+    const bool mine = wr < p.rows_per_cta && r < rows;
     constexpr int NV = (D / 4 + 31) / 32;               // float4 columns per lane
-    for (int r = (int)blockIdx.y * p.rows_per_cta; r < r_end; ++r) {
-        float m = -INFINITY, l = 0.f;
-        float4 acc[NV] = {};
-        for (int w = w0 + warp; w <= w1; w += kJoinWarps) {
-            const int slot = w == w0 ? slot0 : 2 * w;
-            const float2 x = __ldcg(&p.part_ml[slot * 16 + r]);
-            float4 v[NV];
+    float m = -INFINITY, l = 0.f;
+    float4 acc[NV] = {};
+    if (mine) {
+        for (int wb = w0 + ws; wb <= w1; wb += split * kJoinUnroll) {
+            float2 x[kJoinUnroll];
+            float4 v[kJoinUnroll][NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i * 32 + lane < D / 4)
-                    v[i] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + ((size_t)slot * 16 + r) * D) + i * 32 + lane);
-            const float mn = fmaxf(m, x.x);
-            const float z = mn == -INFINITY ? 0.f : mn;
-            const float a = exp2f(m - z), c = exp2f(x.x - z);
+            for (int u = 0; u < kJoinUnroll; ++u) {
+                const int w = wb + u * split;
+                const size_t slot = (size_t)(w == w0 ? slot0 : 2 * w) * 16 + r;
+                x[u] = w <= w1 ? __ldcg(&p.part_ml[slot]) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    v[u][i] = (w <= w1 && i * 32 + lane < D / 4)
+                                  ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot * D) + i * 32 + lane)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mn = m;
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; ++u) mn = fmaxf(mn, x[u].x);
+            const float z = mn == -INFINITY ? 0.f : mn, a = ex2(m - z);
             m = mn;
-            l = l * a + x.y * c;
+            l *= a;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (i * 32 + lane < D / 4) {
-                    acc[i].x = acc[i].x * a + v[i].x * c;
-                    acc[i].y = acc[i].y * a + v[i].y * c;
-                    acc[i].z = acc[i].z * a + v[i].z * c;
-                    acc[i].w = acc[i].w * a + v[i].w * c;
+                acc[i].x *= a;
+                acc[i].y *= a;
+                acc[i].z *= a;
+                acc[i].w *= a;
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; ++u) {
+                const float c = ex2(x[u].x - z);
+                l += x[u].y * c;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    acc[i].x += v[u][i].x * c;
+                    acc[i].y += v[u][i].y * c;
+                    acc[i].z += v[u][i].z * c;
+                    acc[i].w += v[u][i].w * c;
                 }
             }
         }
+    }
+    if (split > 1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (i * 32 + lane < D / 4) sum[warp][i * 32 + lane] = acc[i];
         if (lane == 0) ml[warp] = make_float2(m, l);
         __syncthreads();
-        if ((int)threadIdx.x < D / 4) {
-            float mt = -INFINITY;
-            for (int w = 0; w < kJoinWarps; ++w) mt = fmaxf(mt, ml[w].x);
-            const float z = mt == -INFINITY ? 0.f : mt;
-            float lt = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < kJoinWarps; ++w) {
-                const float c = exp2f(ml[w].x - z);
-                const float4 v = sum[w][threadIdx.x];
-                lt += ml[w].y * c;
-                o.x += v.x * c;
-                o.y += v.y * c;
-                o.z += v.z * c;
-                o.w += v.w * c;
+        if (!mine || ws != 0) return;
+        for (int w = 1; w < split; ++w) m = fmaxf(m, ml[warp + w].x);
+        const float z = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < split; ++w) {
+            const float c = ex2(ml[warp + w].x - z);
+            l += ml[warp + w].y * c;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (i * 32 + lane >= D / 4) continue;
+                const float4 v = sum[warp + w][i * 32 + lane];
+                acc[i].x += v.x * c;
+                acc[i].y += v.y * c;
+                acc[i].z += v.z * c;
+                acc[i].w += v.w * c;
             }
-            const float f = lt == 0.f ? 0.f : p.v_scale / lt;
-            T *out = reinterpret_cast<T *>(p.O) + b * p.o_row + (long long)(h * p.group + qt * 16 + r) * p.o_head;
-            *reinterpret_cast<uint2 *>(out + 4 * threadIdx.x) = make_uint2(pack2<T>(o.x * f, o.y * f), pack2<T>(o.z * f, o.w * f));
-            if (p.lse && threadIdx.x == 0)
-                p.lse[(long long)b * p.heads + h * p.group + qt * 16 + r] =
-                    lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.693147180559945309f;
         }
-        __syncthreads();
     }
+    if (!mine) return;
+    const float f = l == 0.f ? 0.f : p.v_scale / l;
+    T *out = reinterpret_cast<T *>(p.O) + b * p.o_row + (long long)(h * p.group + qt * 16 + r) * p.o_head;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (i * 32 + lane < D / 4)
+            *reinterpret_cast<uint2 *>(out + 4 * (i * 32 + lane)) =
+                make_uint2(pack2<T>(acc[i].x * f, acc[i].y * f), pack2<T>(acc[i].z * f, acc[i].w * f));
+    if (p.lse && lane == 0)
+        p.lse[(long long)b * p.heads + h * p.group + qt * 16 + r] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
 // ------------------------------------------------------------------ host side
@@ -756,10 +866,24 @@ wsm_status run_attention(const AttnParams &p, int dev, int sms, cudaStream_t str
     return op_launch(&attention_join_kernel<T, D>, join_grid, kJoinWarps * 32, 0, stream, p);
 }
 
-int attention_warps(int head_dim) { return head_dim >= 256 ? 4 : 8; }
+int attention_warps(int head_dim, bool e4m3) {
+    switch (head_dim) {
+        case 64: return e4m3 ? AttnGeo<64, 1>::kWarps : AttnGeo<64, 2>::kWarps;
+        case 96: return e4m3 ? AttnGeo<96, 1>::kWarps : AttnGeo<96, 2>::kWarps;
+        case 128: return e4m3 ? AttnGeo<128, 1>::kWarps : AttnGeo<128, 2>::kWarps;
+        default: return e4m3 ? AttnGeo<256, 1>::kWarps : AttnGeo<256, 2>::kWarps;
+    }
+}
 
-size_t attention_ws(int batch, int head_dim, int sms) {
-    const size_t slots = (size_t)sms * attention_warps(head_dim) * 2;
+// No item can be cut when none can have more than kSnapGroups groups.
+bool attention_may_cut(long long max_tokens, int window) {
+    const long long span = window > 0 ? std::min<long long>(max_tokens, (long long)window + kGroup - 1) : max_tokens;
+    return (span + kGroup - 1) / kGroup > kSnapGroups;
+}
+
+// Partials of two items per range (the first and the last it holds a part of), and the prefix sums.
+size_t attention_ws(int batch, int head_dim, bool e4m3, int sms) {
+    const size_t slots = (size_t)sms * attention_warps(head_dim, e4m3) * 2;
     return slots * 16 * (size_t)head_dim * 4 + slots * 16 * 8 + ((size_t)batch + 1 + 3) / 4 * 16;
 }
 
@@ -835,15 +959,19 @@ wsm_status wsm_paged_cache_append(const wsm_kv_cache *cache, const wsm_kv_rows *
     return op_launch(&append_kernel<__half, false>, grid, kAppendThreads, 0, stream, p);  // a copy: any 16-bit type
 }
 
-size_t wsm_paged_attention_workspace_bytes(int batch, int head_dim) {
-    if (batch < 0 || batch > kMaxBatch || !attention_dim_ok(head_dim)) {
-        op_fail(WSM_ERR_UNSUPPORTED, "paged attention takes up to %d sequences and head dimensions 64, 96, 128 and 256 (got %d, %d)",
-                kMaxBatch, batch, head_dim);
-        return 0;
-    }
+wsm_status wsm_paged_attention_workspace(int batch, int head_dim, int cache_dtype, long long max_tokens, int window,
+                                         size_t *bytes) {
+    if (!bytes) return op_fail(WSM_ERR_INVALID, "bytes must be non-null");
+    if (batch < 0 || max_tokens < 0 || window < 0) return op_fail(WSM_ERR_INVALID, "sizes must not be negative");
+    if (batch > kMaxBatch || !attention_dim_ok(head_dim))
+        return op_fail(WSM_ERR_UNSUPPORTED, "paged attention takes up to %d sequences and head dimensions 64, 96, 128 and 256 (got %d, %d)",
+                       kMaxBatch, batch, head_dim);
+    *bytes = 0;
+    if (batch == 0 || !attention_may_cut(max_tokens, window)) return WSM_OK;
     int dev, sms;
-    if (device_sms(&dev, &sms) != WSM_OK) return 0;
-    return attention_ws(batch, head_dim, sms);
+    wsm_status st = device_sms(&dev, &sms);
+    if (st == WSM_OK) *bytes = attention_ws(batch, head_dim, cache_dtype == WSM_DTYPE_E4M3, sms);
+    return st;
 }
 
 wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a, wsm_stream_t stream_) {
@@ -864,11 +992,13 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
         return op_fail(WSM_ERR_INVALID, "%d query heads are not a multiple of %d key-value heads", a->heads, cache->kv_heads);
     if (a->batch > kMaxBatch) return op_fail(WSM_ERR_UNSUPPORTED, "%d sequences: up to %d are", a->batch, kMaxBatch);
     const long long max_tokens = (long long)a->max_pages * cache->page_size;
-    if (max_tokens > 0x7fffffffll - kGroup || (max_tokens / kGroup + 1) * std::max(a->batch, 1) > 0x7fffffffll)
+    if (max_tokens > 0x7fffffffll - kGroup || (max_tokens / kGroup + 1 + kItemCost) * std::max(a->batch, 1) * ((long long)cache->kv_heads * ((a->heads / cache->kv_heads + 15) / 16)) > 0x7fffffffll)
         return op_fail(WSM_ERR_UNSUPPORTED, "%d sequences of up to %lld tokens are too many", a->batch, max_tokens);
     if (!(a->scale > -INFINITY) || !(a->scale < INFINITY)) return op_fail(WSM_ERR_INVALID, "the scale must be finite");
     if (a->batch == 0) return WSM_OK;
-    if (!a->Q || !a->O || !a->lengths || (!a->block_table && a->max_pages > 0) || !a->workspace)
+    const bool e8 = cache->dtype == WSM_DTYPE_E4M3;
+    const bool join = attention_may_cut(max_tokens, a->window);
+    if (!a->Q || !a->O || !a->lengths || (!a->block_table && a->max_pages > 0) || (!a->workspace && join))
         return op_fail(WSM_ERR_INVALID, "Q, O, lengths, block_table and workspace must be non-null device pointers");
     if (!aligned_to(a->Q, 16) || !aligned_to(a->O, 16) || !aligned_to(a->workspace, 16))
         return op_fail(WSM_ERR_ALIGN, "Q, O and workspace must be 16-byte aligned");
@@ -884,7 +1014,7 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     if (a->batch > 1 && a->table_stride < 0) return op_fail(WSM_ERR_INVALID, "the table stride must not be negative");
     int dev, sms;
     if ((st = device_sms(&dev, &sms)) != WSM_OK) return st;
-    const size_t need = attention_ws(a->batch, cache->head_dim, sms);
+    const size_t need = join ? attention_ws(a->batch, cache->head_dim, e8, sms) : 0;
     if (a->workspace_bytes < need)
         return op_fail(WSM_ERR_NOMEM, "workspace of %zu bytes is smaller than the %zu needed", a->workspace_bytes, need);
 
@@ -897,11 +1027,13 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     p.lse = a->lse;
     p.table = a->block_table;
     p.lengths = a->lengths;
-    p.workers = sms * attention_warps(D);
-    const size_t slots = (size_t)p.workers * 2;
-    p.part_o = static_cast<float *>(a->workspace);
-    p.part_ml = reinterpret_cast<float2 *>(p.part_o + slots * 16 * (size_t)D);
-    p.prefix = reinterpret_cast<int *>(p.part_ml + slots * 16);
+    p.workers = sms * attention_warps(D, e8);
+    if (join) {
+        const size_t slots = (size_t)p.workers * 2;
+        p.part_o = static_cast<float *>(a->workspace);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + slots * 16 * (size_t)D);
+        p.prefix = reinterpret_cast<int *>(p.part_ml + slots * 16);
+    }
     p.q_row = step_of(a->q_strides[0], n_q[0]);
     p.q_head = step_of(a->q_strides[1], n_q[1]);
     p.o_row = step_of(a->o_strides[0], n_q[0]);
@@ -922,18 +1054,26 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     p.group = a->heads / cache->kv_heads;
     p.q_tiles = (p.group + 15) / 16;
     p.page_size = cache->page_size;
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (cache->page_size == (1 << i)) p.page_shift = i;
+    const double reach = std::max(((double)cache->num_pages - 1) * p.k_page + ((double)cache->page_size - 1) * p.k_tok +
+                                      ((double)cache->kv_heads - 1) * p.k_head,
+                                  ((double)cache->num_pages - 1) * p.v_page + ((double)cache->page_size - 1) * p.v_tok +
+                                      ((double)cache->kv_heads - 1) * p.v_head);
+    p.far = reach * (e8 ? 1 : 2) / 16 >= 4294967295.0;
+    p.kv_alike = p.k_page == p.v_page && p.k_tok == p.v_tok && p.k_head == p.v_head;
     p.max_tokens = (int)max_tokens;
     p.window = a->window;
-    // no item can be cut when none can have more than kSnapGroups groups
-    const long long span = a->window > 0 ? std::min<long long>(max_tokens, (long long)a->window + kGroup - 1) : max_tokens;
-    const bool join = (span + kGroup - 1) / kGroup > kSnapGroups;
     const long long items = (long long)p.batch * p.kv_heads * p.q_tiles;
     if (items > 0x7fffffffll) return op_fail(WSM_ERR_UNSUPPORTED, "%lld items are too many", items);
     const int rows = std::min(16, p.group);
-    p.rows_per_cta = items * rows <= 8ll * sms ? 1 : rows;
+    // a block for each row while there are few (and may be many partials), else one for all of an item's
+    p.rows_per_cta = items * rows <= 2ll * sms ? 1 : rows;
+    p.join_split = kJoinWarps / p.rows_per_cta;
     const dim3 jg((unsigned)items, (unsigned)((rows + p.rows_per_cta - 1) / p.rows_per_cta));
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    const bool bf = a->dtype == WSM_DTYPE_BF16, e8 = cache->dtype == WSM_DTYPE_E4M3;
+    const bool bf = a->dtype == WSM_DTYPE_BF16;
 #define WSM_ATTN(DIM)                                                                                             \
     case DIM:                                                                                                     \
         if (e8)                                                                                                   \

@@ -39,13 +39,6 @@ struct LogprobsParams {
     int ctas;                       // blocks per row
 };
 
-// 2^y: the hardware approximation, relative error 2^-22, subnormal results 0 (next to a sum of 1 or more)
-__device__ __forceinline__ float ex2(float y) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
-    return e;
-}
-
 // Running statistics of some of a row's elements: the largest so far (-infinity: none yet), l and u relative
 // to it.  Differences are taken before the factor log2 e: the type's lowest value times it is not a number.
 struct Stat {

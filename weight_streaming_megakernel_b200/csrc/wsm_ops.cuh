@@ -105,6 +105,13 @@ __device__ __forceinline__ void record_op_error(int *status, int code, int which
     }
 }
 
+// 2^y: the hardware approximation, relative error 2^-22, subnormal results 0
+__device__ __forceinline__ float ex2(float y) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    return e;
+}
+
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }

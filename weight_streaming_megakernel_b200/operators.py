@@ -6,6 +6,10 @@ checked, packed into the C structs of ``include/wsm.h`` and handed to the
 library's kernels.  Outputs and scratch come from torch's allocator on the
 call's stream, so calls on other streams and captured graphs share nothing.
 Tensors must lie on one device; it need not be the current one.
+
+A call's time on the host is the whole cost of the smallest ones, so each
+checks its tensors in one expression; only when that fails does a second,
+slower pass find out what to say.
 """
 from __future__ import annotations
 
@@ -19,7 +23,11 @@ import torch
 import weight_streaming_megakernel_b200 as _wsm
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
-_BF16, _FP16, _FP32, _E4M3 = range(4)
+_E4M3 = 3
+_ROW_TYPES = (torch.bfloat16, torch.float16)
+_CACHE_TYPES = (torch.bfloat16, torch.float16, torch.float8_e4m3fn)
+_LOGIT_TYPES = (torch.float32, torch.bfloat16, torch.float16)
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 # wsm_kv_cache, wsm_kv_rows, wsm_attention, wsm_experts, wsm_logprobs
 _CACHE = struct.Struct("@2P6qq4i2f")
@@ -28,7 +36,8 @@ _ATTENTION = struct.Struct("@5P5qPN5if")
 _EXPERTS = struct.Struct("@5P4qPN6i")
 _LOGPROBS = struct.Struct("@6Pq4i")
 
-_INT_MAX = 2**31 - 1
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 class TokenLogprobs(NamedTuple):
@@ -40,100 +49,67 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: torch.Tensor  # [rows, top] fp32
 
 
-def _tensor(name, t, dims, device=None, dtype=None):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(shape)}")
-    if max(shape) > _INT_MAX:
-        raise ValueError(f"{name} is too large: {tuple(shape)}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return shape
+def _elsewhere(op, device: int, stream, *args, **kwargs):
+    """`op` on a device other than the current one, or on a given stream (a
+    torch stream or a raw handle), which is made current around the call so
+    that outputs and scratch are allocated for it."""
+    with torch.cuda.device(device):
+        if stream is None:
+            return op(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device.index != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
+        with torch.cuda.stream(stream):
+            return op(*args, **kwargs)
 
 
-def _dtype(name, t, allowed):
-    code = _DTYPES.get(t.dtype, -1)
-    if code not in allowed:
-        raise TypeError(f"{name} cannot be {t.dtype}")
-    return code
+def _refuse(device: int, *tensors):
+    """What is wrong with a call's tensors: for each (name, tensor, shape with
+    None for any size, types, contiguous in all dimensions).  Always raises."""
+    for name, t, shape, types, whole in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+        if t.dtype not in types:
+            raise TypeError(f"{name} must be {' or '.join(map(str, types))}, got {t.dtype}")
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            raise ValueError(f"{name} must be [{', '.join('any' if n is None else str(n) for n in shape)}], "
+                             f"got {list(t.shape)}")
+        if whole and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    raise ValueError("the tensors do not fit one another")
 
 
-def _output(name, t, shape, device, dtype):
-    """A caller's contiguous output buffer."""
-    _tensor(name, t, len(shape), device, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _shape(t, dims):
+    """A tensor's shape where it has `dims` dimensions, else Nones."""
+    return tuple(t.shape) if isinstance(t, torch.Tensor) and t.dim() == dims else (None,) * dims
 
 
-def _on_stream(op):
-    """`op` runs on the current stream of its tensors' device.  With stream=
-    (a torch stream or a raw handle) that stream is made current around the
-    call, so that outputs and scratch are allocated for it; likewise a device
-    other than the current one."""
-
-    @functools.wraps(op)
-    def call(first, *args, stream=None, **kwargs):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            return op(first, *args, **kwargs)  # its own checks say what is wrong
-        index = first.device.index
-        if stream is None and index == torch.cuda.current_device():
-            return op(first, *args, **kwargs)
-        with torch.cuda.device(index):
-            if stream is None:
-                return op(first, *args, **kwargs)
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=first.device)
-            if stream.device.index != index:
-                raise ValueError(f"the stream belongs to {stream.device}, the tensors to {first.device}")
-            with torch.cuda.stream(stream):
-                return op(first, *args, **kwargs)
-
-    return call
+def _device_of(t) -> int:
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
-def _current(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _types_of(t, types):
+    """The types that go with `t`'s."""
+    return (t.dtype,) if isinstance(t, torch.Tensor) and t.dtype in types else types
 
 
-@functools.lru_cache(maxsize=4096)
-def _attention_bytes(device_index: int, batch: int, head_dim: int) -> int:
-    n = _wsm.lib().wsm_paged_attention_workspace_bytes(batch, head_dim)
-    if n == 0:
-        raise _wsm.WsmError(_wsm.WSM_ERR_UNSUPPORTED, "wsm_paged_attention_workspace_bytes", _wsm.last_error())
-    return n
+def _pack_cache(k_cache, v_cache, k_scale, v_scale, code):
+    pages, page, heads, dim = k_cache.shape
+    k0, k1, k2, _ = k_cache.stride()
+    v0, v1, v2, _ = v_cache.stride()
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, pages, page, heads, dim, code,
+                       k_scale, v_scale)
 
 
-@functools.lru_cache(maxsize=4096)
-def _experts_bytes(device_index: int, rows: int, experts: int) -> int:
-    n = _wsm.lib().wsm_expert_gemm_workspace_bytes(rows, experts)
-    if n == 0:
-        raise _wsm.WsmError(_wsm.WSM_ERR_UNSUPPORTED, "wsm_expert_gemm_workspace_bytes", _wsm.last_error())
-    return n
-
-
-def _pack_cache(k_cache, v_cache, k_scale, v_scale, device):
-    pages, page, heads, dim = shape = _tensor("k_cache", k_cache, 4, device)
-    if _tensor("v_cache", v_cache, 4, device, k_cache.dtype) != shape:
-        raise ValueError(f"k_cache {tuple(shape)} and v_cache {tuple(v_cache.shape)} differ in shape")
-    code = _dtype("k_cache", k_cache, (_BF16, _FP16, _E4M3))
-    ks, vs = k_cache.stride(), v_cache.stride()
-    return shape, code, _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                                    pages, page, heads, dim, code, k_scale, v_scale)
-
-
-@_on_stream
 def paged_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
-                       slots: torch.Tensor, *, k_scale: float = 1.0, v_scale: float = 1.0) -> None:
+                       slots: torch.Tensor, *, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Write new tokens' keys and values into their slots of a paged cache.
 
     k, v: [tokens, kv_heads, head_dim] bf16 or fp16, any strides that are
@@ -143,26 +119,49 @@ def paged_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
     three dimensions.  slots: [tokens] int64, page * page_size + place in the
     page; negative: the row is skipped.  Slots of one call must differ.
     """
-    device = k.device if isinstance(k, torch.Tensor) else None
-    tokens, heads, dim = shape = _tensor("k", k, 3)
-    if _tensor("v", v, 3, device, k.dtype) != shape:
-        raise ValueError(f"k {tuple(shape)} and v {tuple(v.shape)} differ in shape")
-    cache_shape, _, cache = _pack_cache(k_cache, v_cache, k_scale, v_scale, device)
-    if cache_shape[2:] != shape[1:]:
-        raise ValueError(f"k {tuple(shape)} does not fit a cache of {tuple(cache_shape)}")
-    if _tensor("slots", slots, 1, device, torch.int64) != (tokens,):
-        raise ValueError(f"slots must be [{tokens}]")
-    ks, vs = k.stride(), v.stride()
-    rows = _ROWS.pack(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], slots.data_ptr(), tokens,
-                      _dtype("k", k, (_BF16, _FP16)))
-    _wsm._check(_wsm.lib().wsm_paged_cache_append(cache, rows, _current(device)), "wsm_paged_cache_append")
+    device = _device_of(k)
+    try:
+        shape, cache_shape = k.shape, k_cache.shape
+        dtype, cache_dtype = k.dtype, k_cache.dtype
+        k0, k1, k2 = k.stride()
+        v0, v1, v2 = v.stride()
+        fits = (device >= 0 and device == v.get_device() == k_cache.get_device() == v_cache.get_device()
+                == slots.get_device() and dtype in _ROW_TYPES and dtype == v.dtype and v_cache.dtype == cache_dtype
+                and (cache_dtype == dtype or cache_dtype == torch.float8_e4m3fn) and slots.dtype == _I64
+                and v.shape == shape and v_cache.shape == cache_shape and cache_shape[2:] == shape[1:]
+                and len(cache_shape) == 4 and slots.shape == shape[:1] and slots.is_contiguous()
+                and (shape[2] == 1 or k2 == v2 == k_cache.stride(3) == v_cache.stride(3) == 1))
+    except (AttributeError, ValueError, TypeError, IndexError):
+        fits = False
+    if not fits:
+        tokens, heads, dim = _shape(k, 3)
+        pages, page = _shape(k_cache, 4)[:2]
+        one = _types_of(k, _ROW_TYPES)
+        cached = _types_of(k_cache, one + (torch.float8_e4m3fn,))
+        _refuse(device, ("k", k, (None,) * 3, _ROW_TYPES, False), ("v", v, (tokens, heads, dim), one, False),
+                ("k_cache", k_cache, (None, None, heads, dim), one + (torch.float8_e4m3fn,), False),
+                ("v_cache", v_cache, (pages, page, heads, dim), cached, False), ("slots", slots, (tokens,), (_I64,), True))
+    if stream is not None or device != _current_device():
+        return _elsewhere(paged_cache_append, device, stream, k, v, k_cache, v_cache, slots, k_scale=k_scale, v_scale=v_scale)
+    cache = _pack_cache(k_cache, v_cache, k_scale, v_scale, _DTYPES[cache_dtype])
+    rows = _ROWS.pack(k.data_ptr(), v.data_ptr(), k0, k1, v0, v1, slots.data_ptr(), shape[0], _DTYPES[dtype])
+    code = _wsm.lib().wsm_paged_cache_append(cache, rows, _current_stream(device))
+    if code:
+        _wsm._check(code, "wsm_paged_cache_append")
 
 
-@_on_stream
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(device: int, batch: int, head_dim: int, code: int, max_tokens: int, window: int) -> int:
+    n = ctypes.c_size_t(0)
+    _wsm._check(_wsm.lib().wsm_paged_attention_workspace(batch, head_dim, code, max_tokens, window, ctypes.byref(n)),
+                "wsm_paged_attention_workspace")
+    return n.value
+
+
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                     lengths: torch.Tensor, out: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
                     window: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
-                    lse: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of one new token of each sequence over a paged cache.
 
     q: [batch, heads, head_dim] bf16 or fp16 (heads a multiple of the cache's
@@ -174,41 +173,65 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     only.  lse: optional [batch, heads] fp32 buffer for the logarithm of the
     softmax's sum.  Returns out, like q (by default a new contiguous tensor).
     """
-    batch, heads, dim = shape = _tensor("q", q, 3)
-    device = q.device
-    code = _dtype("q", q, (_BF16, _FP16))
-    cache_shape, cache_code, cache = _pack_cache(k_cache, v_cache, k_scale, v_scale, device)
-    if cache_shape[3] != dim:
-        raise ValueError(f"q {tuple(shape)} does not fit a cache of {tuple(cache_shape)}")
-    if cache_code != _E4M3 and cache_code != code:
-        raise TypeError(f"q is {q.dtype}, the cache {k_cache.dtype}")
-    table_shape = _tensor("block_table", block_table, 2, device, torch.int32)
-    if table_shape[0] != batch:
-        raise ValueError(f"block_table must have {batch} rows")
-    if _tensor("lengths", lengths, 1, device, torch.int32) != (batch,):
-        raise ValueError(f"lengths must be [{batch}]")
+    device = _device_of(q)
+    try:
+        shape, cache_shape, table_shape = q.shape, k_cache.shape, block_table.shape
+        dtype, cache_dtype = q.dtype, k_cache.dtype
+        batch, heads, dim = shape
+        q0, q1, q2 = q.stride()
+        fits = (device >= 0 and device == k_cache.get_device() == v_cache.get_device() == block_table.get_device()
+                == lengths.get_device() and dtype in _ROW_TYPES and v_cache.dtype == cache_dtype
+                and (cache_dtype == dtype or cache_dtype == torch.float8_e4m3fn)
+                and block_table.dtype == lengths.dtype == _I32
+                and v_cache.shape == cache_shape and len(cache_shape) == 4 and cache_shape[3] == dim
+                and len(table_shape) == 2 and table_shape[0] == batch and (table_shape[1] <= 1 or block_table.stride(1) == 1)
+                and lengths.shape == shape[:1] and lengths.is_contiguous()
+                and (dim == 1 or q2 == k_cache.stride(3) == v_cache.stride(3) == 1)
+                and (lse is None or (lse.get_device() == device and lse.dtype == _F32 and lse.shape == shape[:2]
+                                     and lse.is_contiguous()))
+                and (out is None or (out.get_device() == device and out.dtype == dtype and out.shape == shape
+                                     and out.stride(2) == 1)))
+    except (AttributeError, ValueError, TypeError, IndexError):
+        fits = False
+    if not fits:
+        batch, heads, dim = _shape(q, 3)
+        one = _types_of(q, _ROW_TYPES)
+        more = [] if lse is None else [("lse", lse, (batch, heads), (_F32,), True)]
+        more += [] if out is None else [("out", out, (batch, heads, dim), one, False)]
+        pages, page, kv_heads = _shape(k_cache, 4)[:3]
+        _refuse(device, ("q", q, (None,) * 3, _ROW_TYPES, False),
+                ("k_cache", k_cache, (None, None, None, dim), one + (torch.float8_e4m3fn,), False),
+                ("v_cache", v_cache, (pages, page, kv_heads, dim), _types_of(k_cache, one + (torch.float8_e4m3fn,)), False),
+                ("block_table", block_table, (batch, None), (_I32,), False), ("lengths", lengths, (batch,), (_I32,), True), *more)
+    if stream is not None or device != _current_device():
+        return _elsewhere(paged_attention, device, stream, q, k_cache, v_cache, block_table, lengths, out, scale=scale,
+                          window=window, k_scale=k_scale, v_scale=v_scale, lse=lse)
     if out is None:
         out = q.new_empty(shape)
-    elif _tensor("out", out, 3, device, q.dtype) != shape:
-        raise ValueError(f"out must be {list(shape)}")
-    if lse is not None:
-        _output("lse", lse, (batch, heads), device, torch.float32)
-    if batch == 0:
-        return out
-    n = _attention_bytes(device.index, batch, dim)
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    qs, os_ = q.stride(), out.stride()
-    args = _ATTENTION.pack(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else 0,
-                           block_table.data_ptr(), lengths.data_ptr(), qs[0], qs[1], os_[0], os_[1],
-                           block_table.stride(0), ws.data_ptr(), n, batch, heads, table_shape[1], window, code,
-                           dim ** -0.5 if scale is None else scale)
-    _wsm._check(_wsm.lib().wsm_paged_attention(cache, args, _current(device)), "wsm_paged_attention")
+    code = _DTYPES[cache_dtype]
+    n = _attention_bytes(device, batch, dim, code, table_shape[1] * cache_shape[1], window)
+    ws = q.new_empty(n, dtype=torch.uint8) if n else None
+    o0, o1, _ = out.stride()
+    cache = _pack_cache(k_cache, v_cache, k_scale, v_scale, code)
+    args = _ATTENTION.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), block_table.data_ptr(),
+                           lengths.data_ptr(), q0, q1, o0, o1, block_table.stride(0), ws.data_ptr() if n else 0, n,
+                           batch, heads, table_shape[1], window, _DTYPES[dtype], dim ** -0.5 if scale is None else scale)
+    code = _wsm.lib().wsm_paged_attention(cache, args, _current_stream(device))
+    if code:
+        _wsm._check(code, "wsm_paged_attention")
     return out
 
 
-@_on_stream
+@functools.lru_cache(maxsize=4096)
+def _experts_bytes(device: int, rows: int, experts: int) -> int:
+    n = _wsm.lib().wsm_expert_gemm_workspace_bytes(rows, experts)
+    if n == 0:
+        raise _wsm.WsmError(_wsm.WSM_ERR_UNSUPPORTED, "wsm_expert_gemm_workspace_bytes", _wsm.last_error())
+    return n
+
+
 def expert_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: Optional[torch.Tensor] = None, *,
-                epilogue: int = 0, row_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
+                epilogue: int = 0, row_scale: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Products grouped by expert: y[r] = x[r] @ w[e].T for the rows
     offsets[e] <= r < offsets[e + 1] of expert e; returns y.
 
@@ -219,33 +242,48 @@ def expert_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: Opti
     weights).  Rows outside all experts are left as they were: in a new y
     they are undefined.
     """
-    rows, k = _tensor("x", x, 2)
-    device = x.device
-    code = _dtype("x", x, (_BF16, _FP16))
-    experts, n, wk = _tensor("w", w, 3, device, x.dtype)
-    if wk != k:
-        raise ValueError(f"shapes x{tuple(x.shape)} w{tuple(w.shape)} do not form x[rows, K] . w[e][N, K]^T")
-    if _tensor("offsets", offsets, 1, device, torch.int32) != (experts + 1,):
-        raise ValueError(f"offsets must be [{experts + 1}]")
-    shape = (rows, n // 2 if epilogue == _wsm.EPI_SILU_MUL else n)
+    device = _device_of(x)
+    try:
+        dtype = x.dtype
+        rows, k = x.shape
+        experts, n, wk = w.shape
+        x0, x1 = x.stride()
+        w0, w1, w2 = w.stride()
+        cols = n // 2 if epilogue == 1 else n
+        fits = (device >= 0 and device == w.get_device() == offsets.get_device() and dtype in _ROW_TYPES and w.dtype == dtype
+                and offsets.dtype == _I32 and wk == k and offsets.shape == (experts + 1,) and offsets.is_contiguous()
+                and (k == 1 or x1 == w2 == 1)
+                and (row_scale is None or (row_scale.get_device() == device and row_scale.dtype == _F32
+                                           and row_scale.shape == (rows,) and row_scale.is_contiguous()))
+                and (y is None or (y.get_device() == device and y.dtype == dtype and y.shape == (rows, cols)
+                                   and (cols == 1 or y.stride(1) == 1))))
+    except (AttributeError, ValueError, TypeError, IndexError):
+        fits = False
+    if not fits:
+        rows, k = _shape(x, 2)
+        experts, n, _ = _shape(w, 3)
+        one = _types_of(x, _ROW_TYPES)
+        more = [] if row_scale is None else [("row_scale", row_scale, (rows,), (_F32,), True)]
+        more += [] if y is None else [("y", y, (rows, n if n is None or epilogue != 1 else n // 2), one, False)]
+        _refuse(device, ("x", x, (None, None), _ROW_TYPES, False), ("w", w, (None, None, k), one, False),
+                ("offsets", offsets, (None if experts is None else experts + 1,), (_I32,), True), *more)
+    if stream is not None or device != _current_device():
+        return _elsewhere(expert_gemm, device, stream, x, w, offsets, y, epilogue=epilogue, row_scale=row_scale)
     if y is None:
-        y = x.new_empty(shape)
-    elif _tensor("y", y, 2, device, x.dtype) != shape:
-        raise ValueError(f"y must be {list(shape)}")
-    if row_scale is not None and _tensor("row_scale", row_scale, 1, device, torch.float32) != (rows,):
-        raise ValueError(f"row_scale must be [{rows}]")
-    nbytes = _experts_bytes(device.index, rows, experts)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    we, wr, _ = w.stride()
+        y = x.new_empty((rows, cols))
+    nbytes = _experts_bytes(device, rows, experts)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
     args = _EXPERTS.pack(x.data_ptr(), w.data_ptr(), y.data_ptr(), offsets.data_ptr(),
-                         row_scale.data_ptr() if row_scale is not None else 0, x.stride(0), we, wr, y.stride(0),
-                         ws.data_ptr(), nbytes, rows, experts, n, k, epilogue, code)
-    _wsm._check(_wsm.lib().wsm_expert_gemm(args, _current(device)), "wsm_expert_gemm")
+                         0 if row_scale is None else row_scale.data_ptr(), x0, w0, w1, y.stride(0), ws.data_ptr(), nbytes,
+                         rows, experts, n, k, epilogue, _DTYPES[dtype])
+    code = _wsm.lib().wsm_expert_gemm(args, _current_stream(device))
+    if code:
+        _wsm._check(code, "wsm_expert_gemm")
     return y
 
 
-@_on_stream
-def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top: int = 0) -> TokenLogprobs:
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top: int = 0,
+                   stream=None) -> TokenLogprobs:
     """Log probabilities of given tokens, the entropy of each row's
     distribution and its `top` (at most 32) likeliest tokens.
 
@@ -255,19 +293,30 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     first, equal ones by the lower index; places that no token with a
     probability above 0 takes hold -1 and -infinity.
     """
-    rows, vocab = _tensor("logits", logits, 2)
-    device = logits.device
-    code = _dtype("logits", logits, (_FP32, _BF16, _FP16))
-    if tokens is not None and _tensor("tokens", tokens, 1, device, torch.int64) != (rows,):
-        raise ValueError(f"tokens must be [{rows}]")
-    both = torch.empty((2, rows), dtype=torch.float32, device=device)
-    logprob, entropy = both[0], both[1]
-    top_lp = torch.empty((rows, max(top, 0)), dtype=torch.float32, device=device)
-    top_ids = torch.empty((rows, max(top, 0)), dtype=torch.int64, device=device)
-    at = both.data_ptr()
-    args = _LOGPROBS.pack(logits.data_ptr(), tokens.data_ptr() if tokens is not None else 0, at, at + 4 * rows,
-                          top_ids.data_ptr(), top_lp.data_ptr(), logits.stride(0), rows, vocab, top, code)
-    _wsm._check(_wsm.lib().wsm_token_logprobs(args, _current(device)), "wsm_token_logprobs")
+    device = _device_of(logits)
+    try:
+        dtype = logits.dtype
+        rows, vocab = logits.shape
+        x0, x1 = logits.stride()
+        fits = (device >= 0 and dtype in _LOGIT_TYPES and (vocab == 1 or x1 == 1)
+                and (tokens is None or (tokens.get_device() == device and tokens.dtype == _I64 and tokens.shape == (rows,)
+                                        and tokens.is_contiguous())))
+    except (AttributeError, ValueError, TypeError, IndexError):
+        fits = False
+    if not fits:
+        more = [] if tokens is None else [("tokens", tokens, _shape(logits, 2)[:1], (_I64,), True)]
+        _refuse(device, ("logits", logits, (None, None), _LOGIT_TYPES, False), *more)
+    if stream is not None or device != _current_device():
+        return _elsewhere(token_logprobs, device, stream, logits, tokens, top=top)
+    width = top if top > 0 else 0
+    logprob, entropy = logits.new_empty((2, rows), dtype=_F32)
+    top_lp = logits.new_empty((rows, width), dtype=_F32)
+    top_ids = logits.new_empty((rows, width), dtype=_I64)
+    args = _LOGPROBS.pack(logits.data_ptr(), 0 if tokens is None else tokens.data_ptr(), logprob.data_ptr(),
+                          entropy.data_ptr(), top_ids.data_ptr(), top_lp.data_ptr(), x0, rows, vocab, top, _DTYPES[dtype])
+    code = _wsm.lib().wsm_token_logprobs(args, _current_stream(device))
+    if code:
+        _wsm._check(code, "wsm_token_logprobs")
     return TokenLogprobs(logprob, entropy, top_ids, top_lp)
 
 
