@@ -4,8 +4,14 @@
 // With m = max x, y_j = (x_j - m) log2 e, l = sum 2^y_j and u = sum 2^y_j y_j, all in one pass:
 //     logprob(t) = (x_t - m) - ln 2 log2 l,    entropy = ln 2 (log2 l - u / l).
 // A thread keeps m, l and u of its elements and rescales them when its maximum moves; parts join exactly by
-// the same rule.  The alternatives come from the same pass: each warp keeps its best 32 in order, one to a
-// lane, and an element is looked at again only if it beats the warp's k-th best (and the block's best k-th).
+// the same rule.
+//
+// The alternatives: at least k elements reach the k-th largest of the block's 256 threads' maxima, and few more
+// do.  A thread remembers where its maximum was and how large its other blocks got, so after the pass the threads
+// that reach that floor read one block of theirs again (now and then all of them), and the elements found are
+// ranked by counting.  Where that finds too many -- thousands of equal values, or nearly all of a row masked --
+// the block goes through its part once more with a sorted list of the best 32 in each warp's lanes, which is
+// slower and has no such case.
 //
 // What bounds it is reading the logits once.  A row goes to one block, or with few rows to a cluster of up
 // to eight, whose parts meet in the first one's shared memory: no scratch and one launch.
@@ -23,7 +29,9 @@ static __device__ int g_logprobs_status[kOpStatusInts];
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;         // one alternative per lane of a warp's list
-constexpr int kLpUnroll = 4;        // 16-byte loads of a thread's block of elements
+constexpr int kLpLoads = 8;         // 16-byte loads of a thread in a turn over the row
+constexpr int kLpUnroll = 4;        // ... and how many of them it unpacks at a time
+constexpr int kFound = 512;         // elements that reach the floor there is room for
 constexpr int kMaxCluster = 8;      // the portable cluster size
 
 constexpr float kLog2e = 1.44269504088896341f;
@@ -39,26 +47,28 @@ struct LogprobsParams {
     int ctas;                       // blocks per row
 };
 
-// Running statistics of some of a row's elements: the largest so far (-infinity: none yet), l and u relative
-// to it.  Differences are taken before the factor log2 e: the type's lowest value times it is not a number.
+// Running statistics of some of a row's elements: the largest so far (-infinity: none yet), and l and u relative
+// to r = m log2 e, rounded: y is one operation, x log2 e - r, off by the same rounding for all elements, which
+// logprobs take back.  For a maximum past kFar that rounding would no longer be small (nor r a number, for the
+// type's lowest value); there elements go by far_y, two operations.
+constexpr float kFar = 65536.f;
 struct Stat {
-    float m, l, u;
+    float m, r, l, u;
 };
+__device__ __forceinline__ float base_of(float m) { return fminf(fmaxf(m, -kFar), kFar) * kLog2e; }
+// y of an element by a maximum past kFar: differences of the elements themselves, as anything else vanishes
+__device__ __forceinline__ float far_y(float x, float m) { return (x - m) * kLog2e; }
 // l and u move to a larger maximum; nothing summed so far (or a weight that vanishes) leaves nothing.
-__device__ __forceinline__ void rebase(float &l, float &u, float from, float to) {
-    const float d = fmaxf((from - to) * kLog2e, -200.f), f = ex2(d);
-    u = (u + l * d) * f;
-    l *= f;
+__device__ __forceinline__ void rebase(Stat &s, float m) {
+    const bool far = fabsf(m) > kFar || fabsf(s.m) > kFar;
+    const float r = base_of(m);
+    const float d = fmaxf(far ? far_y(s.m, m) : s.r - r, -200.f), f = ex2(d);
+    s.u = (s.u + s.l * d) * f;
+    s.l *= f;
+    s.m = m;
+    s.r = r;
 }
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-    Stat s;
-    s.m = fmaxf(a.m, b.m);
-    if (a.m < s.m) rebase(a.l, a.u, a.m, s.m);
-    if (b.m < s.m) rebase(b.l, b.u, b.m, s.m);
-    s.l = a.l + b.l;
-    s.u = a.u + b.u;
-    return s;
-}
+__device__ __forceinline__ Stat no_elements() { return Stat{-INFINITY, -kFar * kLog2e, 0.f, 0.f}; }
 
 // Order-preserving key of a value and its place: larger value first, then the lower index.  -0 is 0; 0 is no
 // element's key.
@@ -97,21 +107,6 @@ struct TopList {
     }
 };
 
-// The k-th largest of the warp's 32 values.
-__device__ __forceinline__ float kth_of_warp(float v, int k) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-        for (int j = size >> 1; j > 0; j >>= 1) {
-            const float w = __shfl_xor_sync(0xffffffffu, v, j);
-            const bool desc = (lane & size) == 0, low = (lane & j) == 0;
-            v = (low == desc) ? fmaxf(v, w) : fminf(v, w);
-        }
-    }
-    return __shfl_sync(0xffffffffu, v, k - 1);
-}
-
 template <typename T, int VEC> __device__ __forceinline__ void unpack_vec(const uint4 &v, float *x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -126,164 +121,333 @@ template <typename T, int VEC> __device__ __forceinline__ void unpack_vec(const 
     }
 }
 
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
-    constexpr int VEC = 16 / (int)sizeof(T);
-    constexpr int NB = kLpUnroll * VEC;                 // elements of a thread's block
-    __shared__ Stat warp_stat[kLpWarps];
-    __shared__ unsigned long long warp_top[kTop ? kLpWarps : 1][kMaxTop];
-    __shared__ unsigned long long best[kMaxTop];
-    // what the row's blocks bring to the first one
-    __shared__ Stat all_stat[kMaxCluster];
-    __shared__ unsigned long long all_top[kTop ? kMaxCluster : 1][kMaxTop];
-    __shared__ int shared_least;                        // order-preserving bits of the warps' best k-th value
+// The largest of a vector's elements (NaN left aside), and a vector of -infinities.
+template <typename T> struct Vec16;
+template <> struct Vec16<float> {
+    static constexpr uint32_t kNone = 0xff800000u;
+    static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpUnroll]) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kLpUnroll; ++i)
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y)),
+                               fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w))));
+        return m;
+    }
+};
+template <typename T2> __device__ __forceinline__ T2 word_as(uint32_t w) { return *reinterpret_cast<T2 *>(&w); }
+template <typename T2> __device__ __forceinline__ T2 max_of_words(const uint4 (&v)[kLpUnroll]) {
+    T2 m = word_as<T2>(v[0].x);
+#pragma unroll
+    for (int i = 0; i < kLpUnroll; ++i)
+        m = __hmax2(m, __hmax2(__hmax2(word_as<T2>(v[i].x), word_as<T2>(v[i].y)), __hmax2(word_as<T2>(v[i].z), word_as<T2>(v[i].w))));
+    return m;
+}
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr uint32_t kNone = 0xff80ff80u;
+    static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpUnroll]) {
+        const float2 f = __bfloat1622float2(max_of_words<__nv_bfloat162>(v));
+        return fmaxf(f.x, f.y);
+    }
+};
+template <> struct Vec16<__half> {
+    static constexpr uint32_t kNone = 0xfc00fc00u;
+    static __device__ __forceinline__ float max_of(const uint4 (&v)[kLpUnroll]) {
+        const float2 f = __half22float2(max_of_words<__half2>(v));
+        return fmaxf(f.x, f.y);
+    }
+};
 
+// Where a block's part of a row lies: elements before the first 16-byte boundary (the first block's), whole
+// vectors (dealt to the row's blocks in consecutive stretches), and the rest (the last block's).
+template <typename T> struct RowPart {
+    static constexpr int VEC = 16 / (int)sizeof(T);
+    static constexpr int kStep = kLpThreads * kLpLoads; // vectors a block takes per turn
+    const T *x;
+    const uint4 *vec;
+    int head, tail0, vocab, v_begin, v_end, turns;
+    bool first, last;
+    __device__ __forceinline__ RowPart(const LogprobsParams &p, long long row, int part) {
+        x = reinterpret_cast<const T *>(p.logits) + row * p.stride;
+        vocab = p.vocab;
+        head = min(vocab, (int)(((16u - (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / sizeof(T)));
+        const int n_vec = (vocab - head) / VEC;
+        tail0 = head + n_vec * VEC;
+        const int share = (n_vec + p.ctas - 1) / p.ctas;
+        v_begin = min(n_vec, part * share);
+        v_end = min(n_vec, v_begin + share);
+        vec = reinterpret_cast<const uint4 *>(x + head);
+        turns = (v_end - v_begin + kStep - 1) / kStep;
+        first = part == 0;
+        last = part == p.ctas - 1;
+    }
+    // load i of a thread in a turn: a warp's vectors ascend from turn to turn and from load to load
+    __device__ __forceinline__ int vector_at(int turn, int i) const {
+        return v_begin + turn * kStep + (int)(threadIdx.x >> 5) * (32 * kLpLoads) + i * 32 + (int)(threadIdx.x & 31);
+    }
+};
+
+// Whole numbers in the order of the values (-0 is 0), and back.
+__device__ __forceinline__ int ordered_int(float x) {
+    const int b = __float_as_int(x + 0.f);
+    return b < 0 ? b ^ 0x7fffffff : b;
+}
+__device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b < 0 ? b ^ 0x7fffffff : b); }
+
+// The best p.top of a block's part by sorted lists: every element is offered to its warp's.  Leaves them in
+// best[], best first.  All threads.
+template <typename T>
+__device__ __noinline__ void top_by_lists(const RowPart<T> &r, int k, unsigned long long (*warp_top)[kMaxTop],
+                                          unsigned long long *best) {
+    constexpr int VEC = RowPart<T>::VEC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = p.ctas > 1 ? (int)cluster_ctarank() : 0;
-    const long long row = (long long)blockIdx.x / p.ctas;
-    if (kTop && threadIdx.x < kMaxTop) best[threadIdx.x] = 0ull;
-    if (threadIdx.x == 0) shared_least = (int)0x80000000;
-    __syncthreads();
-    if (p.ctas > 1) cluster_sync_all();                 // every block of the row is there to be written to
-    pdl_wait();
-    pdl_launch_dependents();
-
-    // The row: elements before the first 16-byte boundary, whole vectors (dealt to the row's blocks in
-    // consecutive stretches), and the rest.
-    const T *x_row = reinterpret_cast<const T *>(p.logits) + row * p.stride;
-    const int head = min(p.vocab, (int)(((16u - (uint32_t)(reinterpret_cast<uintptr_t>(x_row) & 15u)) & 15u) / sizeof(T)));
-    const int n_vec = (p.vocab - head) / VEC;
-    const int tail0 = head + n_vec * VEC;
-    const int share = (n_vec + p.ctas - 1) / p.ctas;
-    const int v_begin = min(n_vec, part * share), v_end = min(n_vec, v_begin + share);
-    const uint4 *vec = reinterpret_cast<const uint4 *>(x_row + head);
-
-    Stat st = {-INFINITY, 0.f, 0.f};
-    float base = 0.f;                                   // what y is counted from: the largest so far, or 0
     TopList top;
     top.key = 0ull;
     top.least = -INFINITY;
-    top.k = p.top;
-
-    auto raise = [&](float bm) {                        // bm > st.m: the maximum moves
-        rebase(st.l, st.u, st.m, bm);
-        st.m = base = bm;
+    top.k = k;
+    auto single = [&](bool have, int index) {
+        const float x = have ? to_f32<T>(r.x[index]) : -INFINITY;
+        top.offer(x > top.least, x, index);
     };
-    auto add = [&](float x, float &l, float &u) {
-        const float y = (x - base) * kLog2e;
-        const float e = ex2(y);
-        l += e;
-        u = fmaf(e, fmaxf(y, -200.f), u);               // (-infinity: weight 0 times a finite number)
-    };
-    auto single = [&](bool have, int index) {           // one element per lane: a row's ragged ends
-        const float x = have ? to_f32<T>(x_row[index]) : -INFINITY;
-        if (x > st.m) raise(x);
-        add(x, st.l, st.u);
-        if constexpr (kTop) top.offer(x > top.least, x, index);
-    };
-    if (part == 0 && warp == 0 && head > 0) single(lane < head, lane);
-
-    uint4 cur[kLpUnroll];
-    constexpr int kStep = kLpThreads * kLpUnroll;       // vectors a block takes per turn
-    // a warp's vectors ascend from turn to turn and, within one, from load to load
-    int v0 = v_begin + warp * (32 * kLpUnroll) + lane;
-    auto load = [&](int at, uint4 (&r)[kLpUnroll]) {
-#pragma unroll
-        for (int i = 0; i < kLpUnroll; ++i)
-            if (at + i * 32 < v_end) r[i] = __ldcs(vec + at + i * 32);
-    };
-    load(v0, cur);
-    bool fresh = true;                                  // no block of this warp seen yet
-    const int turns = (v_end - v_begin + kStep - 1) / kStep;
-    for (int turn = 0; turn < turns; ++turn) {
-        uint4 next[kLpUnroll];
-        load(v0 + kStep, next);
-        float x[NB];
-#pragma unroll
-        for (int i = 0; i < kLpUnroll; ++i) {
-            if (v0 + i * 32 < v_end) {
-                unpack_vec<T, VEC>(cur[i], &x[i * VEC]);
+    if (r.first && warp == 0 && r.head > 0) single(lane < r.head, lane);
+    for (int turn = 0; turn < r.turns; ++turn) {
+#pragma unroll 1
+        for (int i = 0; i < kLpLoads; ++i) {
+            const int v = r.vector_at(turn, i);
+            float x[VEC];
+            if (v < r.v_end) {
+                unpack_vec<T, VEC>(r.vec[v], x);
             } else {
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) x[i * VEC + j] = -INFINITY;
+                for (int j = 0; j < VEC; ++j) x[j] = -INFINITY;
             }
+            // an element equal to the least of a full list comes later in the row than all that are listed, unless
+            // it is one of this vector's
+            const float over = top.least;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) top.offer(x[j] > over, x[j], r.head + v * VEC + j);
         }
-        float bm = x[0];
+    }
+    if (r.last && warp == kLpWarps - 1 && r.tail0 < r.vocab) single(r.tail0 + lane < r.vocab, r.tail0 + lane);
+    warp_top[warp][lane] = lane < k ? top.key : 0ull;
+    if (threadIdx.x < kMaxTop) best[threadIdx.x] = 0ull;
+    __syncthreads();
+    // an entry's place is the number of larger ones (no two are equal)
+    const unsigned long long mine = warp_top[warp][lane];
+    int rank = 0;
+    for (int w = 0; w < kLpWarps; ++w)
+        for (int j = 0; j < k; ++j) rank += warp_top[w][j] > mine ? 1 : 0;
+    if (mine != 0ull && rank < k) best[rank] = mine;
+    __syncthreads();
+}
+
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+    constexpr int VEC = RowPart<T>::VEC;
+    constexpr int NB = kLpUnroll * VEC;                 // elements of a thread's block
+    __shared__ int warp_tops[kLpWarps];
+    __shared__ float2 warp_sums[kLpWarps];
+    __shared__ unsigned long long best[kMaxTop];
+    // what the row's blocks bring to the first one
+    __shared__ __align__(16) Stat all_stat[kMaxCluster];
+    __shared__ unsigned long long all_top[kTop ? kMaxCluster : 1][kMaxTop];
+    __shared__ __align__(16) float thread_max[kTop ? kLpThreads : 4];
+    __shared__ unsigned long long found[kTop ? kFound : 1];
+    __shared__ int n_found, floor_of_top;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = p.ctas > 1 ? (int)cluster_ctarank() : 0;
+    const long long row = blockIdx.x / (unsigned)p.ctas;
+    if (p.ctas > 1) cluster_sync_all();                 // every block of the row is there to be written to
+    pdl_wait();
+    pdl_launch_dependents();
+    const RowPart<T> r(p, row, part);
+    // the token asked for and its logit: two loads in a row, well before they are needed
+    long long token = -1;
+    float token_x = 0.f;
+    if (part == 0 && threadIdx.x == 0 && p.tokens) {
+        token = p.tokens[row];
+        if (token >= 0 && token < p.vocab) token_x = to_f32<T>(r.x[token]);
+    }
+
+    Stat st = no_elements();
+    auto single = [&](bool have, int index) {           // one element per lane: a row's ragged ends
+        const float x = have ? to_f32<T>(r.x[index]) : -INFINITY;
+        if (x > st.m) rebase(st, x);
+        if (!(x > -INFINITY) && !(x != x)) return;
+        const float y = fabsf(st.m) > kFar ? far_y(x, st.m) : fmaf(x, kLog2e, -st.r);
+        const float e = ex2(y);
+        st.l += e;
+        st.u = fmaf(e, fmaxf(y, -200.f), st.u);
+    };
+    if (r.first && warp == 0 && r.head > 0) single(lane < r.head, lane);
+    if (r.last && warp == kLpWarps - 1 && r.tail0 < r.vocab) single(r.tail0 + lane < r.vocab, r.tail0 + lane);
+
+    uint4 cur[kLpLoads];
+    auto load = [&](int turn, uint4 (&d)[kLpLoads]) {
+        constexpr uint32_t none = Vec16<T>::kNone;
 #pragma unroll
-        for (int j = 1; j < NB; ++j) bm = fmaxf(bm, x[j]);
-        if (bm > st.m) raise(bm);
-        float l = 0.f, u = 0.f;                         // the block's own sums first: shorter chains of roundings
+        for (int i = 0; i < kLpLoads; ++i) {
+            const int v = r.vector_at(turn, i);
+            d[i] = make_uint4(none, none, none, none);
+            if (v < r.v_end) d[i] = __ldcs(r.vec + v);
+        }
+    };
+    int best_block = -1;                                // where the thread's maximum was (-1: at the ragged ends)
+    float other_max = -INFINITY;                        // the largest of its other blocks' maxima
+    load(0, cur);
+    for (int turn = 0; turn < r.turns; ++turn) {
+        uint4 next[kLpLoads];
+        load(turn + 1, next);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) add(x[j], l, u);
-        st.l += l;
-        st.u += u;
-        if constexpr (kTop) {
-            // Candidates beat the warp's k-th value as it was before this turn: an equal one comes later in
-            // the row than all that are listed.  Against another warp's k-th an equal one may still win.
-            float over = top.least;
-            float from = over;
-            const int sl = *(volatile int *)&shared_least;
-            if (sl != (int)0x80000000) from = fmaxf(from, __int_as_float(sl < 0 ? sl ^ 0x7fffffff : sl));
-            if (fresh) {
-                // the k-th largest of the lanes' maxima is a floor for the k-th element
-                from = fmaxf(from, kth_of_warp(bm, p.top));
-                fresh = false;
+        for (int h = 0; h < kLpLoads; h += kLpUnroll) {
+            uint4 raw[kLpUnroll];
+#pragma unroll
+            for (int i = 0; i < kLpUnroll; ++i) raw[i] = cur[h + i];
+            const float bm = Vec16<T>::max_of(raw);
+            if (bm > st.m) {
+                if (kTop) {
+                    other_max = st.m;
+                    best_block = turn * (kLpLoads / kLpUnroll) + h / kLpUnroll;
+                }
+                rebase(st, bm);
+            } else if (kTop) {
+                other_max = fmaxf(other_max, bm);
             }
-            if (__any_sync(0xffffffffu, bm > over && bm >= from)) {
+            float x[NB];
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    top.offer(x[j] > over && x[j] >= from, x[j],
-                              head + (v0 + (j / VEC) * 32) * VEC + (j % VEC));
-                if (lane == 0 && top.least > -INFINITY) {
-                    const int b = __float_as_int(top.least + 0.f);
-                    atomicMax(&shared_least, b < 0 ? b ^ 0x7fffffff : b);
+            for (int i = 0; i < kLpUnroll; ++i) unpack_vec<T, VEC>(raw[i], &x[i * VEC]);
+            // the block's own sums first: shorter chains of roundings
+            float l = 0.f, u = 0.f;
+            if (fabsf(st.m) <= kFar || st.m == -INFINITY) {
+                const float r0 = st.m == -INFINITY ? 0.f : st.r;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const float y = fmaf(x[j], kLog2e, -r0), e = ex2(y);
+                    l += e;
+                    u = fmaf(e, fmaxf(y, -200.f), u);   // (-infinity: weight 0 times a finite number)
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kLpUnroll; ++i) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        const float y = far_y(x[j], st.m), e = ex2(y);
+                        l += e;
+                        u = fmaf(e, fmaxf(y, -200.f), u);
+                    }
+#pragma unroll
+                    for (int j = 0; j + VEC < NB; ++j) x[j] = x[j + VEC];
                 }
             }
+            st.l += l;
+            st.u += u;
         }
 #pragma unroll
-        for (int i = 0; i < kLpUnroll; ++i) cur[i] = next[i];
-        v0 += kStep;
-    }
-    if (part == p.ctas - 1 && warp == kLpWarps - 1 && tail0 < p.vocab)
-        single(tail0 + lane < p.vocab, tail0 + lane);
-
-    // ---- the warp's, the block's, the row's statistics
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stat b;
-        b.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        b.l = __shfl_xor_sync(0xffffffffu, st.l, o);
-        b.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-        st = join(st, b);
-    }
-    if (lane == 0) warp_stat[warp] = st;
-    if constexpr (kTop) warp_top[warp][lane] = lane < p.top ? top.key : 0ull;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kLpWarps; ++w) st = join(st, warp_stat[w]);
-        if (part == 0) {
-            all_stat[0] = st;
-        } else {
-            const uint32_t a = map_to_rank(smem_u32(&all_stat[part]), 0);
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(st.m) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 4), "f"(st.l) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(st.u) : "memory");
-        }
+        for (int i = 0; i < kLpLoads; ++i) cur[i] = next[i];
     }
     if constexpr (kTop) {
-        // an entry's place is the number of larger ones (no two are equal); the best p.top of the block
-        const unsigned long long mine = warp_top[warp][lane];
-        int rank = 0;
-        for (int w = 0; w < kLpWarps; ++w)
-            for (int j = 0; j < p.top; ++j) rank += warp_top[w][j] > mine ? 1 : 0;
-        if (mine != 0ull && rank < p.top) best[rank] = mine;
-        __syncthreads();
-        if (p.ctas > 1) {
-            if (threadIdx.x < kMaxTop) {
-                const uint32_t a = map_to_rank(smem_u32(&all_top[part][threadIdx.x]), 0);
-                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(best[threadIdx.x]) : "memory");
+        thread_max[threadIdx.x] = st.m;
+        if (threadIdx.x < kMaxTop) best[threadIdx.x] = 0ull;
+        if (threadIdx.x == 0) n_found = 0;
+    }
+
+    // ---- the block's maximum; every thread's sums relative to it, added up
+    const float my_max = st.m;
+    const int warp_max = __reduce_max_sync(0xffffffffu, ordered_int(st.m));
+    if (lane == 0) warp_tops[warp] = warp_max;
+    __syncthreads();
+    int block_max = warp_tops[0];
+#pragma unroll
+    for (int w = 1; w < kLpWarps; ++w) block_max = max(block_max, warp_tops[w]);
+    rebase(st, from_ordered(block_max));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        st.l += __shfl_xor_sync(0xffffffffu, st.l, o);
+        st.u += __shfl_xor_sync(0xffffffffu, st.u, o);
+    }
+    if (lane == 0) warp_sums[warp] = make_float2(st.l, st.u);
+    if constexpr (kTop) {
+        // The p.top-th largest of the threads' maxima, to its 16 leading bits and rounded down (a slightly lower floor is
+        // one too): two bits at a time, the largest value that as many of them reach.
+        if (warp == 0) {
+            uint32_t v[kLpWarps], bits = 0u;
+#pragma unroll
+            for (int i = 0; i < kLpWarps; ++i) v[i] = (uint32_t)ordered_int(thread_max[i * 32 + lane]) ^ 0x80000000u;
+#pragma unroll
+            for (int b = 30; b >= 16; b -= 2) {
+                uint32_t reach = 0u;                    // threads that reach each of the three next values, 10 bits each
+#pragma unroll
+                for (int i = 0; i < kLpWarps; ++i)
+                    reach += (v[i] >= (bits | (1u << b)) ? 1u : 0u) + (v[i] >= (bits | (2u << b)) ? 1u << 10 : 0u) +
+                             (v[i] >= (bits | (3u << b)) ? 1u << 20 : 0u);
+                reach = __reduce_add_sync(0xffffffffu, reach);
+                const uint32_t k = (uint32_t)p.top;
+                bits |= (reach >> 20) >= k ? 3u << b : ((reach >> 10) & 1023u) >= k ? 2u << b : (reach & 1023u) >= k ? 1u << b : 0u;
             }
+            static_assert(kLpThreads < 1024, "counts of ten bits");
+            if (lane == 0) floor_of_top = (int)(bits ^ 0x80000000u);
         }
+        __syncthreads();
+        const int least_int = floor_of_top;
+        auto find = [&](float x, int index) {
+            // (the floor of a masked row lies below -infinity, among the NaN)
+            if (ordered_int(x) >= least_int && x > -INFINITY) {
+                const int at = atomicAdd(&n_found, 1);
+                if (at < kFound) found[at] = key_of(x, index);
+            }
+        };
+        if (r.first && warp == 0 && lane < r.head) find(to_f32<T>(r.x[lane]), lane);
+        if (r.last && warp == kLpWarps - 1 && r.tail0 + lane < r.vocab) find(to_f32<T>(r.x[r.tail0 + lane]), r.tail0 + lane);
+        auto look = [&](int v) {
+            if (v >= r.v_end) return;
+            float x[VEC];
+            unpack_vec<T, VEC>(__ldg(r.vec + v), x);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) find(x[j], r.head + v * VEC + j);
+        };
+        constexpr int kPer = kLpLoads / kLpUnroll;      // blocks per turn
+        if (best_block >= 0 && ordered_int(my_max) >= least_int) {
+#pragma unroll
+            for (int i = 0; i < kLpUnroll; ++i) look(r.vector_at(best_block / kPer, best_block % kPer * kLpUnroll + i));
+        }
+        // threads of which another block reaches it: the warp reads all of the thread's vectors, one to a lane
+        uint32_t todo = __ballot_sync(0xffffffffu, other_max > -INFINITY && ordered_int(other_max) >= least_int);
+        // (all lanes go on or stop together)
+        while (todo && !__any_sync(0xffffffffu, *(volatile int *)&n_found > kFound)) {
+            const int src = __ffs((int)todo) - 1;
+            todo &= todo - 1;
+            const int done = __shfl_sync(0xffffffffu, best_block, src);
+            for (int i = lane; i < r.turns * kLpLoads; i += 32)
+                if (i / kLpUnroll != done) look(r.vector_at(i / kLpLoads, i % kLpLoads) + src - lane);
+        }
+        __syncwarp();
+        __syncthreads();
+        const int n = n_found;
+        if (n <= kFound) {
+            // an element's place is the number of larger ones
+            for (int i = threadIdx.x; i < n; i += kLpThreads) {
+                const unsigned long long mine = found[i];
+                int rank = 0;
+                for (int j = 0; j < n; ++j) rank += found[j] > mine ? 1 : 0;
+                if (rank < p.top) best[rank] = mine;
+            }
+            __syncthreads();
+        } else {
+            // (the found elements' memory holds the lists now)
+            top_by_lists<T>(r, p.top, reinterpret_cast<unsigned long long(*)[kMaxTop]>(found), best);
+        }
+        if (p.ctas > 1 && threadIdx.x < kMaxTop) {
+            const uint32_t a = map_to_rank(smem_u32(&all_top[part][threadIdx.x]), 0);
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(best[threadIdx.x]) : "memory");
+        }
+    }
+    if constexpr (!kTop) __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kLpWarps; ++w) {
+            st.l += warp_sums[w].x;
+            st.u += warp_sums[w].y;
+        }
+        st_cluster_v4(map_to_rank(smem_u32(&all_stat[part]), 0), st.m, st.r, st.l, st.u);
     }
     if (p.ctas > 1) {
         cluster_sync_all();                             // the parts are in the first block's shared memory
@@ -293,36 +457,40 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
             if (threadIdx.x < kMaxTop) best[threadIdx.x] = 0ull;
             __syncthreads();
             int rank = 0;
-            for (int w = 0; w < p.ctas; ++w)
-                for (int j = 0; j < p.top; ++j) rank += all_top[w][j] > mine ? 1 : 0;
+            if (lane < p.top)
+                for (int w = 0; w < p.ctas; ++w)
+                    for (int j = 0; j < p.top; ++j) rank += all_top[w][j] > mine ? 1 : 0;
             if (mine != 0ull && rank < p.top) best[rank] = mine;
             __syncthreads();
         }
     }
-    static_assert(kMaxCluster <= kLpWarps, "one warp per block's list");
+    static_assert(kMaxCluster <= kLpWarps && kFound >= kLpWarps * kMaxTop, "one warp per list, and room for the lists");
     if (warp != 0) return;
     __syncwarp();                                       // (all_stat[0] is lane 0's own write)
-    Stat s = {-INFINITY, 0.f, 0.f};
-    if (lane == 0) {
-        s = all_stat[0];
-        for (int c = 1; c < p.ctas; ++c) s = join(s, all_stat[c]);
+    Stat s = lane < p.ctas ? all_stat[lane] : no_elements();
+    rebase(s, from_ordered(__reduce_max_sync(0xffffffffu, ordered_int(s.m))));
+#pragma unroll
+    for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+        s.l += __shfl_xor_sync(0xffffffffu, s.l, o);
+        s.u += __shfl_xor_sync(0xffffffffu, s.u, o);
     }
-    s.m = __shfl_sync(0xffffffffu, s.m, 0);
-    s.l = __shfl_sync(0xffffffffu, s.l, 0);
+    s.l = __shfl_sync(0xffffffffu, s.l, 0);             // (lanes past the blocks hold sums of nothing)
     s.u = __shfl_sync(0xffffffffu, s.u, 0);
     const bool none = s.l == 0.f;                       // no element above -infinity
-    const float from = none ? 0.f : s.m;
     const float log_l = none ? 0.f : log2f(s.l);
-    auto logprob_of = [&](float x) { return (x - from) - log_l * kLn2; };
+    const float from = (fabsf(s.m) > kFar ? 0.f : fmaf(s.m, kLog2e, -s.r)) - log_l;
+    auto logprob_of = [&](float x) {
+        // x - m as it is; ln 2 times the rounding that r holds (see Stat) less the sum's logarithm
+        return none ? -INFINITY : (x - s.m) + from * kLn2;
+    };
     if (lane == 0) {
         if (p.logprob) {
-            const long long t = p.tokens ? p.tokens[row] : -1;
             float lp = 0.f;
-            if (t >= p.vocab) {
+            if (token >= p.vocab) {
                 lp = NAN;
                 record_op_error(g_logprobs_status, kCodeInvalid, (int)row, kSiteToken);
-            } else if (t >= 0) {
-                lp = logprob_of(to_f32<T>(x_row[t]));
+            } else if (token >= 0) {
+                lp = logprob_of(token_x);
             }
             p.logprob[row] = lp;
         }
