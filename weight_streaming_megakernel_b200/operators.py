@@ -8,8 +8,8 @@ call's stream, so calls on other streams and captured graphs share nothing.
 Tensors must lie on one device; it need not be the current one.
 
 A call's time on the host is the whole cost of the smallest ones, so each
-checks its tensors in one expression; only when that fails does a second,
-slower pass find out what to say.
+asks its tensors for what it needs once and checks it in one expression;
+only when that fails does a second, slower pass find out what to say.
 """
 from __future__ import annotations
 
@@ -23,9 +23,8 @@ import torch
 import weight_streaming_megakernel_b200 as _wsm
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
-_E4M3 = 3
+_E4M3 = torch.float8_e4m3fn
 _ROW_TYPES = (torch.bfloat16, torch.float16)
-_CACHE_TYPES = (torch.bfloat16, torch.float16, torch.float8_e4m3fn)
 _LOGIT_TYPES = (torch.float32, torch.bfloat16, torch.float16)
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
@@ -91,21 +90,9 @@ def _shape(t, dims):
     return tuple(t.shape) if isinstance(t, torch.Tensor) and t.dim() == dims else (None,) * dims
 
 
-def _device_of(t) -> int:
-    return t.get_device() if isinstance(t, torch.Tensor) else -1
-
-
 def _types_of(t, types):
     """The types that go with `t`'s."""
     return (t.dtype,) if isinstance(t, torch.Tensor) and t.dtype in types else types
-
-
-def _pack_cache(k_cache, v_cache, k_scale, v_scale, code):
-    pages, page, heads, dim = k_cache.shape
-    k0, k1, k2, _ = k_cache.stride()
-    v0, v1, v2, _ = v_cache.stride()
-    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, pages, page, heads, dim, code,
-                       k_scale, v_scale)
 
 
 def paged_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -119,32 +106,37 @@ def paged_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
     three dimensions.  slots: [tokens] int64, page * page_size + place in the
     page; negative: the row is skipped.  Slots of one call must differ.
     """
-    device = _device_of(k)
+    device = -1
     try:
-        shape, cache_shape = k.shape, k_cache.shape
+        device = k.get_device()
         dtype, cache_dtype = k.dtype, k_cache.dtype
+        tokens, heads, dim = shape = k.shape
+        pages, page, cache_heads, cache_dim = cache_shape = k_cache.shape
         k0, k1, k2 = k.stride()
         v0, v1, v2 = v.stride()
+        kc0, kc1, kc2, kc3 = k_cache.stride()
+        vc0, vc1, vc2, vc3 = v_cache.stride()
+        (n,) = slots.shape
         fits = (device >= 0 and device == v.get_device() == k_cache.get_device() == v_cache.get_device()
-                == slots.get_device() and dtype in _ROW_TYPES and dtype == v.dtype and v_cache.dtype == cache_dtype
-                and (cache_dtype == dtype or cache_dtype == torch.float8_e4m3fn) and slots.dtype == _I64
-                and v.shape == shape and v_cache.shape == cache_shape and cache_shape[2:] == shape[1:]
-                and len(cache_shape) == 4 and slots.shape == shape[:1] and slots.is_contiguous()
-                and (shape[2] == 1 or k2 == v2 == k_cache.stride(3) == v_cache.stride(3) == 1))
-    except (AttributeError, ValueError, TypeError, IndexError):
+                == slots.get_device() and dtype in _ROW_TYPES and dtype is v.dtype and v_cache.dtype is cache_dtype
+                and (cache_dtype is dtype or cache_dtype is _E4M3) and slots.dtype is _I64 and n == tokens
+                and cache_heads == heads and cache_dim == dim and v.shape == shape and v_cache.shape == cache_shape
+                and slots.is_contiguous() and (dim == 1 or k2 == v2 == kc3 == vc3 == 1))
+    except (AttributeError, ValueError, TypeError):
         fits = False
     if not fits:
         tokens, heads, dim = _shape(k, 3)
         pages, page = _shape(k_cache, 4)[:2]
         one = _types_of(k, _ROW_TYPES)
-        cached = _types_of(k_cache, one + (torch.float8_e4m3fn,))
+        cached = _types_of(k_cache, one + (_E4M3,))
         _refuse(device, ("k", k, (None,) * 3, _ROW_TYPES, False), ("v", v, (tokens, heads, dim), one, False),
-                ("k_cache", k_cache, (None, None, heads, dim), one + (torch.float8_e4m3fn,), False),
+                ("k_cache", k_cache, (None, None, heads, dim), one + (_E4M3,), False),
                 ("v_cache", v_cache, (pages, page, heads, dim), cached, False), ("slots", slots, (tokens,), (_I64,), True))
     if stream is not None or device != _current_device():
         return _elsewhere(paged_cache_append, device, stream, k, v, k_cache, v_cache, slots, k_scale=k_scale, v_scale=v_scale)
-    cache = _pack_cache(k_cache, v_cache, k_scale, v_scale, _DTYPES[cache_dtype])
-    rows = _ROWS.pack(k.data_ptr(), v.data_ptr(), k0, k1, v0, v1, slots.data_ptr(), shape[0], _DTYPES[dtype])
+    cache = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), kc0, kc1, kc2, vc0, vc1, vc2, pages, page, heads, dim,
+                        _DTYPES[cache_dtype], k_scale, v_scale)
+    rows = _ROWS.pack(k.data_ptr(), v.data_ptr(), k0, k1, v0, v1, slots.data_ptr(), tokens, _DTYPES[dtype])
     code = _wsm.lib().wsm_paged_cache_append(cache, rows, _current_stream(device))
     if code:
         _wsm._check(code, "wsm_paged_cache_append")
@@ -173,25 +165,28 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     only.  lse: optional [batch, heads] fp32 buffer for the logarithm of the
     softmax's sum.  Returns out, like q (by default a new contiguous tensor).
     """
-    device = _device_of(q)
+    device = -1
     try:
-        shape, cache_shape, table_shape = q.shape, k_cache.shape, block_table.shape
+        device = q.get_device()
         dtype, cache_dtype = q.dtype, k_cache.dtype
-        batch, heads, dim = shape
+        batch, heads, dim = shape = q.shape
+        pages, page, kv_heads, cache_dim = cache_shape = k_cache.shape
         q0, q1, q2 = q.stride()
+        k0, k1, k2, k3 = k_cache.stride()
+        v0, v1, v2, v3 = v_cache.stride()
+        table_rows, max_pages = block_table.shape
+        t0, t1 = block_table.stride()
+        (n,) = lengths.shape
         fits = (device >= 0 and device == k_cache.get_device() == v_cache.get_device() == block_table.get_device()
-                == lengths.get_device() and dtype in _ROW_TYPES and v_cache.dtype == cache_dtype
-                and (cache_dtype == dtype or cache_dtype == torch.float8_e4m3fn)
-                and block_table.dtype == lengths.dtype == _I32
-                and v_cache.shape == cache_shape and len(cache_shape) == 4 and cache_shape[3] == dim
-                and len(table_shape) == 2 and table_shape[0] == batch and (table_shape[1] <= 1 or block_table.stride(1) == 1)
-                and lengths.shape == shape[:1] and lengths.is_contiguous()
-                and (dim == 1 or q2 == k_cache.stride(3) == v_cache.stride(3) == 1)
-                and (lse is None or (lse.get_device() == device and lse.dtype == _F32 and lse.shape == shape[:2]
+                == lengths.get_device() and dtype in _ROW_TYPES and v_cache.dtype is cache_dtype
+                and (cache_dtype is dtype or cache_dtype is _E4M3) and block_table.dtype is lengths.dtype is _I32
+                and batch == table_rows == n and cache_dim == dim and v_cache.shape == cache_shape
+                and (max_pages <= 1 or t1 == 1) and lengths.is_contiguous() and (dim == 1 or q2 == k3 == v3 == 1)
+                and (lse is None or (lse.get_device() == device and lse.dtype is _F32 and lse.shape == (batch, heads)
                                      and lse.is_contiguous()))
-                and (out is None or (out.get_device() == device and out.dtype == dtype and out.shape == shape
+                and (out is None or (out.get_device() == device and out.dtype is dtype and out.shape == shape
                                      and out.stride(2) == 1)))
-    except (AttributeError, ValueError, TypeError, IndexError):
+    except (AttributeError, ValueError, TypeError):
         fits = False
     if not fits:
         batch, heads, dim = _shape(q, 3)
@@ -200,22 +195,25 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         more += [] if out is None else [("out", out, (batch, heads, dim), one, False)]
         pages, page, kv_heads = _shape(k_cache, 4)[:3]
         _refuse(device, ("q", q, (None,) * 3, _ROW_TYPES, False),
-                ("k_cache", k_cache, (None, None, None, dim), one + (torch.float8_e4m3fn,), False),
-                ("v_cache", v_cache, (pages, page, kv_heads, dim), _types_of(k_cache, one + (torch.float8_e4m3fn,)), False),
+                ("k_cache", k_cache, (None, None, None, dim), one + (_E4M3,), False),
+                ("v_cache", v_cache, (pages, page, kv_heads, dim), _types_of(k_cache, one + (_E4M3,)), False),
                 ("block_table", block_table, (batch, None), (_I32,), False), ("lengths", lengths, (batch,), (_I32,), True), *more)
     if stream is not None or device != _current_device():
         return _elsewhere(paged_attention, device, stream, q, k_cache, v_cache, block_table, lengths, out, scale=scale,
                           window=window, k_scale=k_scale, v_scale=v_scale, lse=lse)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        o0, o1 = heads * dim, dim
+    else:
+        o0, o1, _ = out.stride()
     code = _DTYPES[cache_dtype]
-    n = _attention_bytes(device, batch, dim, code, table_shape[1] * cache_shape[1], window)
+    n = _attention_bytes(device, batch, dim, code, max_pages * page, window)
     ws = q.new_empty(n, dtype=torch.uint8) if n else None
-    o0, o1, _ = out.stride()
-    cache = _pack_cache(k_cache, v_cache, k_scale, v_scale, code)
+    cache = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, pages, page, kv_heads, dim, code,
+                        k_scale, v_scale)
     args = _ATTENTION.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), block_table.data_ptr(),
-                           lengths.data_ptr(), q0, q1, o0, o1, block_table.stride(0), ws.data_ptr() if n else 0, n,
-                           batch, heads, table_shape[1], window, _DTYPES[dtype], dim ** -0.5 if scale is None else scale)
+                           lengths.data_ptr(), q0, q1, o0, o1, t0, ws.data_ptr() if n else 0, n, batch, heads, max_pages,
+                           window, _DTYPES[dtype], dim ** -0.5 if scale is None else scale)
     code = _wsm.lib().wsm_paged_attention(cache, args, _current_stream(device))
     if code:
         _wsm._check(code, "wsm_paged_attention")
@@ -242,39 +240,43 @@ def expert_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: Opti
     weights).  Rows outside all experts are left as they were: in a new y
     they are undefined.
     """
-    device = _device_of(x)
+    device = -1
     try:
+        device = x.get_device()
         dtype = x.dtype
         rows, k = x.shape
         experts, n, wk = w.shape
         x0, x1 = x.stride()
         w0, w1, w2 = w.stride()
-        cols = n // 2 if epilogue == 1 else n
-        fits = (device >= 0 and device == w.get_device() == offsets.get_device() and dtype in _ROW_TYPES and w.dtype == dtype
-                and offsets.dtype == _I32 and wk == k and offsets.shape == (experts + 1,) and offsets.is_contiguous()
+        (marks,) = offsets.shape
+        cols = n // 2 if epilogue == _wsm.EPI_SILU_MUL else n
+        fits = (device >= 0 and device == w.get_device() == offsets.get_device() and dtype in _ROW_TYPES and w.dtype is dtype
+                and offsets.dtype is _I32 and wk == k and marks == experts + 1 and offsets.is_contiguous()
                 and (k == 1 or x1 == w2 == 1)
-                and (row_scale is None or (row_scale.get_device() == device and row_scale.dtype == _F32
+                and (row_scale is None or (row_scale.get_device() == device and row_scale.dtype is _F32
                                            and row_scale.shape == (rows,) and row_scale.is_contiguous()))
-                and (y is None or (y.get_device() == device and y.dtype == dtype and y.shape == (rows, cols)
+                and (y is None or (y.get_device() == device and y.dtype is dtype and y.shape == (rows, cols)
                                    and (cols == 1 or y.stride(1) == 1))))
-    except (AttributeError, ValueError, TypeError, IndexError):
+    except (AttributeError, ValueError, TypeError):
         fits = False
     if not fits:
         rows, k = _shape(x, 2)
         experts, n, _ = _shape(w, 3)
         one = _types_of(x, _ROW_TYPES)
         more = [] if row_scale is None else [("row_scale", row_scale, (rows,), (_F32,), True)]
-        more += [] if y is None else [("y", y, (rows, n if n is None or epilogue != 1 else n // 2), one, False)]
+        more += [] if y is None else [("y", y, (rows, n if n is None or epilogue != _wsm.EPI_SILU_MUL else n // 2), one, False)]
         _refuse(device, ("x", x, (None, None), _ROW_TYPES, False), ("w", w, (None, None, k), one, False),
                 ("offsets", offsets, (None if experts is None else experts + 1,), (_I32,), True), *more)
     if stream is not None or device != _current_device():
         return _elsewhere(expert_gemm, device, stream, x, w, offsets, y, epilogue=epilogue, row_scale=row_scale)
     if y is None:
-        y = x.new_empty((rows, cols))
+        y, y0 = x.new_empty((rows, cols)), cols
+    else:
+        y0 = y.stride(0)
     nbytes = _experts_bytes(device, rows, experts)
     ws = x.new_empty(nbytes, dtype=torch.uint8)
     args = _EXPERTS.pack(x.data_ptr(), w.data_ptr(), y.data_ptr(), offsets.data_ptr(),
-                         0 if row_scale is None else row_scale.data_ptr(), x0, w0, w1, y.stride(0), ws.data_ptr(), nbytes,
+                         0 if row_scale is None else row_scale.data_ptr(), x0, w0, w1, y0, ws.data_ptr(), nbytes,
                          rows, experts, n, k, epilogue, _DTYPES[dtype])
     code = _wsm.lib().wsm_expert_gemm(args, _current_stream(device))
     if code:
@@ -293,15 +295,16 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     first, equal ones by the lower index; places that no token with a
     probability above 0 takes hold -1 and -infinity.
     """
-    device = _device_of(logits)
+    device = -1
     try:
+        device = logits.get_device()
         dtype = logits.dtype
         rows, vocab = logits.shape
         x0, x1 = logits.stride()
         fits = (device >= 0 and dtype in _LOGIT_TYPES and (vocab == 1 or x1 == 1)
-                and (tokens is None or (tokens.get_device() == device and tokens.dtype == _I64 and tokens.shape == (rows,)
+                and (tokens is None or (tokens.get_device() == device and tokens.dtype is _I64 and tokens.shape == (rows,)
                                         and tokens.is_contiguous())))
-    except (AttributeError, ValueError, TypeError, IndexError):
+    except (AttributeError, ValueError, TypeError):
         fits = False
     if not fits:
         more = [] if tokens is None else [("tokens", tokens, _shape(logits, 2)[:1], (_I64,), True)]
@@ -309,7 +312,8 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     if stream is not None or device != _current_device():
         return _elsewhere(token_logprobs, device, stream, logits, tokens, top=top)
     width = top if top > 0 else 0
-    logprob, entropy = logits.new_empty((2, rows), dtype=_F32)
+    logprob = logits.new_empty(rows, dtype=_F32)
+    entropy = torch.empty_like(logprob)
     top_lp = logits.new_empty((rows, width), dtype=_F32)
     top_ids = logits.new_empty((rows, width), dtype=_I64)
     args = _LOGPROBS.pack(logits.data_ptr(), 0 if tokens is None else tokens.data_ptr(), logprob.data_ptr(),
