@@ -37,8 +37,7 @@ constexpr int kStages = 4;
 constexpr int kBoxW = kTileN * kBK * 2;
 constexpr int kNarrow = 64;         // up to this many rows a stage holds two K boxes, above one
 constexpr int kNarrowX = kNarrow * kBK * 2;
-constexpr int kXMaps = 9;           // boxes of 256, 128, ... 2, 1 rows
-constexpr int kTopBox = 8;          // 256 = 2^8
+constexpr int kXMaps = 13;          // boxes of 1, 2, 4, 8, 16 and 32, 64, 96 ... 256 rows
 constexpr int kUnitRing = 8;        // units announced ahead: one per stage at most, and the end
 constexpr int kEpiSets = 2;
 constexpr int kExThreads = 64 + kEpiSets * 128;
@@ -60,7 +59,7 @@ constexpr int kHdrBytes = 256;
 
 struct ExpertParams {
     CUtensorMap tmW;                // [experts][N][K], box 128 x 64
-    CUtensorMap tmX[kXMaps];        // [rows][K], boxes 256 >> i rows x 64
+    CUtensorMap tmX[kXMaps];        // [rows][K], boxes box_rows(i) x 64
     void *Y;
     const int *offsets;
     const float *row_scale;
@@ -82,10 +81,15 @@ struct ExpertParams {
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Rows of X a tile of `rows` loads: a power of two up to 8, then whole groups of 8.
-__device__ __forceinline__ int rows_to_load(int rows) {
-    return rows > 4 ? (rows + 7) & ~7 : rows > 2 ? 4 : rows;
+// The box that holds `rows` rows of X, and its height.  One box to a tile: each copy costs the producer thread
+// about as much as the next (8192 rows over 16 experts on a B200: 507 us with a tile's rows in two to four boxes,
+// 450 us in one), and rows beyond the tile's cost no more than their bytes.
+__host__ __device__ inline int box_of(int rows) {
+    int i = 0;
+    while (i < 4 && (1 << i) < rows) ++i;
+    return rows <= 16 ? i : 4 + (rows + 31) / 32;
 }
+__host__ __device__ inline int box_rows(int i) { return i < 5 ? 1 << i : (i - 4) * 32; }
 
 // Tiles along an expert's rows, and the rows of each (cut evenly, a multiple of 16).
 __device__ __forceinline__ int m_tiles_of(int m) { return ceil_div(m, kTileRows); }
@@ -335,10 +339,11 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
                 const int step = t.mrows <= kNarrow ? 2 : 1;
                 // weights with one reader leave L2 first
                 const uint64_t pol_w = p.rec[t.expert].m <= kTileRows ? pol_once : pol_keep;
-                // the rows to load, as box heights: bit i for tmX[i]; rows past them in a narrow tile's MMA width
-                // are what the stage held before, whose sums nobody reads
-                const int load_rows = rows_to_load(t.rows);
-                const uint32_t box_bytes = (uint32_t)(kBoxW + load_rows * kBK * 2);
+                // rows past the box in the MMA's N are what the stage held before, rows in it past the tile's another
+                // expert's: nobody reads their sums
+                const int box = box_of(t.rows);
+                const CUtensorMap *const tmX = &p.tmX[box];
+                const uint32_t box_bytes = (uint32_t)(kBoxW + box_rows(box) * kBK * 2);
                 unit_meta[slot][0] = u;
                 unit_meta[slot][1] = t.mrows;
                 unit_meta[slot][2] = t.k1 - t.k0;
@@ -355,17 +360,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
                     const uint32_t st = ring_u + (uint32_t)(s * kStageBytes);
                     for (int b = 0; b < boxes; ++b) {
                         tma_load_3d(st + b * kBoxW, &p.tmW, &full_bar[s], (k + b) * kBK, t.n0, t.expert, pol_w);
-                        uint32_t xd = st + step * kBoxW + b * kNarrowX;
-                        int at = t.row0;
-#pragma unroll 1
-                        for (int left = load_rows; left > 0;) {
-                            const int i = __clz(left) - (31 - kTopBox);     // the highest box that fits
-                            const int h = kTileRows >> i;
-                            tma_load_2d_at(xd, &p.tmX[i], &full_bar[s], (k + b) * kBK, at, pol_keep);
-                            xd += (uint32_t)(h * kBK * 2);
-                            at += h;
-                            left -= h;
-                        }
+                        tma_load_2d_at(st + step * kBoxW + b * kNarrowX, tmX, &full_bar[s], (k + b) * kBK, t.row0, pol_keep);
                     }
                     ++issued;
                     if (++s == kStages) {
@@ -611,12 +606,10 @@ wsm_status wsm_expert_gemm(const wsm_experts *a, wsm_stream_t stream_) {
         const cuuint32_t box[3] = {kBK, kTileN, 1};
         if ((st = encode_tiled(&p.tmW, type, 3, a->W, dims, strides, box)) != WSM_OK) return st;
     }
-    const int most = (std::min(a->rows, kTileRows) + 15) / 16 * 16;
-    for (int i = 0; i < kXMaps; ++i) {
-        if ((kTileRows >> i) > most) continue;          // no tile is that high
+    for (int i = 0; i <= box_of(std::min(a->rows, kTileRows)); ++i) {   // no tile is higher
         const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)a->rows};
         const cuuint64_t strides[1] = {(cuuint64_t)xs * 2};
-        const cuuint32_t box[2] = {kBK, (cuuint32_t)(kTileRows >> i)};
+        const cuuint32_t box[2] = {kBK, (cuuint32_t)box_rows(i)};
         if ((st = encode_tiled(&p.tmX[i], type, 2, a->X, dims, strides, box)) != WSM_OK) return st;
     }
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
