@@ -106,8 +106,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // For a sequence of n tokens, a query head and the keys and values of the head it shares:
 //     s_j = scale * k_scale * q . k_j,  m = max s_j,  l = sum e^(s_j - m),
 //     o = v_scale / l * sum e^(s_j - m) v_j,  lse = m + ln l
-// in one pass over the cache: a running maximum and sum, and an output that is rescaled when the maximum
-// moves.  Parts of a sequence computed apart have (m, l, o) of their own and join exactly by the same rule.
+// in one pass over the cache: weights relative to a reference that follows the running maximum, and a sum and
+// output that are rescaled when it moves.  The reference moves only when the maximum has left it by 2^kReach: a
+// warp's first dozens of groups would otherwise rescale every other time.  Parts of a sequence computed apart have
+// a (reference, sum, output) of their own and join exactly by the same rule.
 //
 // What bounds it is reading the cache once.  So the work is cut by cache bytes, not by sequences: the
 // groups of kGroup tokens of all (sequence, key-value head, query tile) items, laid end to end, are dealt
@@ -126,6 +128,9 @@ constexpr int kSnapGroups = 8;      // items of up to this many groups (128 toke
 // What beginning and ending an item costs a warp, in groups: counted when the work is dealt out, so that a warp
 // with many short sequences does not finish last.
 constexpr int kItemCost = 3;
+// Weights are 2^(score - reference), the reference kBelow under the maximum when it is set: so a weight of 2^-31 of
+// the largest is still an fp16 number, and the largest, 2^15, is one too.
+constexpr float kBelow = 7.f, kReach = 15.f;
 
 struct AttnParams {
     const uint8_t *Q;
@@ -134,13 +139,14 @@ struct AttnParams {
     float *lse;
     const int *table, *lengths;
     float *part_o;                  // [workers][2][16][D]
-    float2 *part_ml;                // [workers][2][16]: running maximum (base 2) and sum
+    float2 *part_ml;                // [workers][2][16]: reference (base 2) and sum
     int *prefix;                    // [batch + 1] copy for the join
     long long q_row, q_head, o_row, o_head;        // elements
     long long k_page, k_tok, k_head, v_page, v_tok, v_head;
     long long table_stride;
     long long num_pages;
-    float sl2;                      // scale * k_scale * log2(e)
+    float sl2;                      // |scale| * k_scale * log2(e), not 0
+    int negate;                     // the scale is negative
     float v_scale;
     int batch, heads, kv_heads, group, q_tiles;    // group = heads / kv_heads
     int page_size, page_shift, max_tokens, window; // page_shift: log2 of page_size, or -1
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         for (int i = 0; i < kGroup * CH / 32; ++i) {
             const int idx = i * 32 + lane;
             const int row = idx / CH, ch = idx % CH;
-            const uint32_t bytes = ((mask >> row) & 1u) ? 16u : 0u;
+            const uint32_t bytes = ((mask >> row) << 4) & 16u;
             const uint32_t dst = st + (uint32_t)(row * Geo::kRow + ch * 16);
             unsigned long long rk = __shfl_sync(0xffffffffu, k_lo, half + row);
             if (p.far) rk |= (unsigned long long)__shfl_sync(0xffffffffu, k_hi, half + row) << 32;
@@ -458,6 +464,12 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             qa[ks][2] = g < rows ? *reinterpret_cast<const uint32_t *>(q + g * p.q_head + c1) : 0u;
             qa[ks][3] = g + 8 < rows ? *reinterpret_cast<const uint32_t *>(q + (g + 8) * p.q_head + c1) : 0u;
         }
+        if (p.negate) {                                 // (a negative scale: the factor stays positive)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qa[ks][i] ^= 0x80008000u;
+        }
         f0 = f1 = p.sl2;
         if constexpr (kE4m3 && std::is_same<T, __nv_bfloat16>::value) {
             float a0 = 0.f, a1 = 0.f;
@@ -485,8 +497,8 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
                     qa[ks][2 * i] = pack2<M>(ldexpf(u.x, e0), ldexpf(u.y, e0));
                     qa[ks][2 * i + 1] = pack2<M>(ldexpf(w.x, e1), ldexpf(w.y, e1));
                 }
-            f0 = ldexpf(p.sl2, -e0);
-            f1 = ldexpf(p.sl2, -e1);
+            f0 = fmaxf(ldexpf(p.sl2, -e0), 1e-37f);
+            f1 = fmaxf(ldexpf(p.sl2, -e1), 1e-37f);
         }
 #pragma unroll
         for (int i = 0; i < 2 * KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -542,7 +554,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             }
             if (p.lse && t == 0) {
                 float *lse = p.lse + (long long)cb * p.heads + h * p.group + qt * 16;
-                // the running maximum is in base 2; no finite score at all leaves l = 0 and -infinity
+                // the reference is in base 2; no finite score at all leaves l = 0 and -infinity
                 if (g < rows) lse[g] = (l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * 0.693147180559945309f);
                 if (g + 8 < rows) lse[g + 8] = (l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * 0.693147180559945309f);
             }
@@ -622,12 +634,9 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         }
         float x0[4], x1[4];                             // row g, row g + 8
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                x0[nt * 2 + j] = (s[0][nt][j] + s[1][nt][j]) * f0;
-                x1[nt * 2 + j] = (s[0][nt][2 + j] + s[1][nt][2 + j]) * f1;
-            }
+        for (int j = 0; j < 4; ++j) {
+            x0[j] = s[0][j >> 1][j & 1] + s[1][j >> 1][j & 1];
+            x1[j] = s[0][j >> 1][2 + (j & 1)] + s[1][j >> 1][2 + (j & 1)];
         }
         if (mask != 0xffffu) {
 #pragma unroll
@@ -637,17 +646,18 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
                 x1[j] = in ? x1[j] : -INFINITY;
             }
         }
-        float n0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3]));
-        float n1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3]));
+        float n0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3])) * f0;
+        float n1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3])) * f1;
+        // (a thread of a row's four sees its own four scores: the vote is over all, the maximum is shared only then)
+        if (__any_sync(0xffffffffu, n0 > m0 + kReach || n1 > m1 + kReach)) {
 #pragma unroll
-        for (int x = 1; x < 4; x <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
-            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
-        }
-        if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-            n0 = fmaxf(n0, m0);
-            n1 = fmaxf(n1, m1);
-            // (a maximum still at -infinity has summed nothing yet)
+            for (int x = 1; x < 4; x <<= 1) {
+                n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
+                n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
+            }
+            n0 = n0 > m0 + kReach ? n0 - kBelow : m0;
+            n1 = n1 > m1 + kReach ? n1 - kBelow : m1;
+            // (a reference still at -infinity has summed nothing yet)
             const float a0 = n0 == m0 ? 1.f : ex2(m0 - n0), a1 = n1 == m1 ? 1.f : ex2(m1 - n1);
             m0 = n0;
             m1 = n1;
@@ -664,8 +674,8 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x0[j] = ex2(x0[j] - z0);
-            x1[j] = ex2(x1[j] - z1);
+            x0[j] = ex2(fmaf(x0[j], f0, -z0));
+            x1[j] = ex2(fmaf(x1[j], f1, -z1));
             l0 += x0[j];
             l1 += x1[j];
         }
@@ -1046,7 +1056,9 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     p.v_head = step_of(cache->v_strides[2], n_c[2]);
     p.table_stride = step_of(a->table_stride, a->batch);
     p.num_pages = cache->num_pages;
-    p.sl2 = (float)((double)a->scale * cache->k_scale * 1.44269504088896340736);
+    // (a scale of 0 would make NaN of what is masked; scores times this vanish next to one another all the same)
+    p.sl2 = std::max((float)(std::fabs((double)a->scale) * cache->k_scale * 1.44269504088896340736), 1e-37f);
+    p.negate = a->scale < 0.f;
     p.v_scale = cache->v_scale;
     p.batch = a->batch;
     p.heads = a->heads;
