@@ -107,9 +107,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 //     s_j = scale * k_scale * q . k_j,  m = max s_j,  l = sum e^(s_j - m),
 //     o = v_scale / l * sum e^(s_j - m) v_j,  lse = m + ln l
 // in one pass over the cache: weights relative to a reference that follows the running maximum, and a sum and
-// output that are rescaled when it moves.  The reference moves only when the maximum has left it by 2^kReach: a
-// warp's first dozens of groups would otherwise rescale every other time.  Parts of a sequence computed apart have
-// a (reference, sum, output) of their own and join exactly by the same rule.
+// output that are rescaled when it moves.  Parts of a sequence computed apart have a (reference, sum, output) of
+// their own and join exactly by the same rule.
 //
 // What bounds it is reading the cache once.  So the work is cut by cache bytes, not by sequences: the
 // groups of kGroup tokens of all (sequence, key-value head, query tile) items, laid end to end, are dealt
@@ -128,9 +127,11 @@ constexpr int kSnapGroups = 8;      // items of up to this many groups (128 toke
 // What beginning and ending an item costs a warp, in groups: counted when the work is dealt out, so that a warp
 // with many short sequences does not finish last.
 constexpr int kItemCost = 3;
-// Weights are 2^(score - reference), the reference kBelow under the maximum when it is set: so a weight of 2^-31 of
-// the largest is still an fp16 number, and the largest, 2^15, is one too.
-constexpr float kBelow = 7.f, kReach = 15.f;
+// Weights are 2^(score - reference), the reference kBelow under the running maximum: so a weight of 2^-31 of the
+// largest is still an fp16 number, and the largest is a power of two, which no rounding touches -- where one token
+// has nearly all the weight, the output is its value.  (A reference that moves only when the maximum has left it by
+// far saves most rescalings, 2 % of a call over an 8-bit cache, but rounds the largest weight: errors 1.3 times.)
+constexpr float kBelow = 7.f;
 
 struct AttnParams {
     const uint8_t *Q;
@@ -649,14 +650,14 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         float n0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3])) * f0;
         float n1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3])) * f1;
         // (a thread of a row's four sees its own four scores: the vote is over all, the maximum is shared only then)
-        if (__any_sync(0xffffffffu, n0 > m0 + kReach || n1 > m1 + kReach)) {
+        if (__any_sync(0xffffffffu, n0 > m0 + kBelow || n1 > m1 + kBelow)) {
 #pragma unroll
             for (int x = 1; x < 4; x <<= 1) {
                 n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
                 n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
             }
-            n0 = n0 > m0 + kReach ? n0 - kBelow : m0;
-            n1 = n1 > m1 + kReach ? n1 - kBelow : m1;
+            n0 = n0 > m0 + kBelow ? n0 - kBelow : m0;
+            n1 = n1 > m1 + kBelow ? n1 - kBelow : m1;
             // (a reference still at -infinity has summed nothing yet)
             const float a0 = n0 == m0 ? 1.f : ex2(m0 - n0), a1 = n1 == m1 ? 1.f : ex2(m1 - n1);
             m0 = n0;
