@@ -271,7 +271,8 @@ wsm_status wsm_workspace_status(const void *workspace, size_t workspace_bytes, w
                                 int *code);
 
 /* Test hook, not for real use: each of the next `calls` launches of any entry
- * point (a hybrid chain launches one kernel per part) makes its CTA 0 wait on
+ * point with device-side waits (the GEMMs and chains -- a hybrid chain launches
+ * one kernel per part -- and wsm_expert_gemm) makes its CTA 0 wait on
  * a flag that nothing ever sets for `limit_ns` (at most 10 s), then record
  * WSM_ERR_TIMEOUT and abandon its work -- a device-side time-out on demand,
  * with no fault: every other wait stays bounded and the kernel ends.  calls =
@@ -633,7 +634,8 @@ wsm_status wsm_paged_cache_append(const wsm_kv_cache *cache, const wsm_kv_rows *
  *  - A page number outside [0, num_pages) within a sequence's length: its
  *    tokens are left out, and that is recorded.  Entries past a sequence's last
  *    page are not read, nor are cache slots past its length.
- *  - head_dim 64, 96, 128 or 256.  Results do not depend on timing. */
+ *  - head_dim 64, 96, 128 or 256; batch * kv_heads * ceil(G / 16) * (max_pages
+ *    * page_size / 16 + 4) below 2^31.  Results do not depend on timing. */
 typedef struct {
     const void *Q;           /* [batch, heads, head_dim], strides {sequence, head}, multiples of 16 bytes */
     void *O;                 /* the same shape; its own strides */
@@ -665,6 +667,7 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
  *  - Rows before offsets[0] or from offsets[experts] on are left as they were.
  *  - offsets are read clamped to [0, rows] and never falling (an offset below
  *    an earlier one is taken as that one); what had to be mended is recorded.
+ *  - Y does not overlap X or W.
  *  - Tiles cut across CTAs are added in K order: results do not depend on timing. */
 typedef struct {
     const void *X;           /* [rows, K], 16-byte aligned */

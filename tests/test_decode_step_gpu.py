@@ -124,3 +124,35 @@ def test_step_in_a_graph():
         step.check(s, f"replay {i}")
         step.lengths += (step.lengths > 0).int()
         step.h.normal_()
+
+
+FIRST = """
+import torch, weight_streaming_megakernel_b200 as wsm
+z = lambda *s, dtype=torch.bfloat16: torch.ones(s, dtype=dtype, device="cuda:0")
+k, kc, t, n = z(2, 2, 64), z(40, 16, 2, 64), torch.arange(40, dtype=torch.int32, device="cuda:0").view(2, 20), z(2, dtype=torch.int32) * 300
+x, w, off, ids = z(6, 128), z(2, 64, 128), torch.tensor([0, 3, 6], dtype=torch.int32, device="cuda:0"), z(2, dtype=torch.int64)
+logits = z(2, 70000, dtype=torch.float32)
+calls = dict(append=lambda: wsm.paged_cache_append(k, k, kc, kc.clone(), ids), attention=lambda: wsm.paged_attention(k, kc, kc, t, n),
+             experts=lambda: wsm.expert_gemm(x, w, off), logprobs=lambda: wsm.token_logprobs(logits, ids, top=3))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = calls["%s"]()
+g.replay()
+torch.cuda.synchronize()
+assert wsm.operator_status() == 0
+if "%s" == "attention": assert (out == 1).all()
+if "%s" == "experts": assert (out == 128).all()
+if "%s" == "logprobs": assert out.top_ids.tolist() == [[0, 1, 2]] * 2
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("call", ["append", "attention", "experts", "logprobs"])
+def test_first_call_of_a_process_may_be_captured(call):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST.replace("%s", call)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
