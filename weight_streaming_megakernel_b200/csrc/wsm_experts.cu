@@ -14,7 +14,7 @@
 //   been cleared before.
 //   experts_kernel (persistent, one CTA per SM) claims units in order -- SMs do not stream at one rate -- and
 //   runs them: warp 0 loads by TMA into a ring of four 48 KB stages, warp 1 issues tcgen05.mma into one of two
-//   accumulators in tensor memory, warps 2-5 take finished ones out: activation, scale, rounding, stores.  A
+//   accumulators in tensor memory, warps 2-9 take finished ones out: activation, scale, rounding, stores.  A
 //   tile cut along K leaves fp32 partials, which its last unit to finish adds in K order, so results do not
 //   depend on which SM ran what.
 #include "wsm_ops.cuh"
@@ -38,7 +38,9 @@ constexpr int kBoxW = kTileN * kBK * 2;
 constexpr int kNarrow = 64;         // up to this many rows a stage holds two K boxes, above one
 constexpr int kNarrowX = kNarrow * kBK * 2;
 constexpr int kXMaps = 13;          // boxes of 1, 2, 4, 8, 16 and 32, 64, 96 ... 256 rows
-constexpr int kUnitRing = 8;        // units announced ahead: one per stage at most, and the end
+// Units announced: the one that the producer writes, one to each of the four stages before it, and the two whose
+// accumulators may not have been read.
+constexpr int kUnitRing = 8;
 constexpr int kEpiSets = 2;
 constexpr int kExThreads = 64 + kEpiSets * 128;
 constexpr uint32_t kExTmemCols = 2 * kTileRows;
@@ -53,7 +55,7 @@ struct ExpertRec {
     int nu, ku;                     // units of each split tile, K boxes of a unit
     int mrows;                      // rows per tile, a multiple of 16
 };
-// Head of the scratch: [0] units, [1] tiles before the split ones, [2] claim counter, [3] experts that have rows + 1 ...
+// Head of the scratch: [0] units, [1] tiles before the split ones, [2] claim counter.
 enum : int { kHdrUnits = 0, kHdrHead = 1, kHdrClaim = 2 };
 constexpr int kHdrBytes = 256;
 
@@ -91,7 +93,7 @@ __host__ __device__ inline int box_of(int rows) {
 }
 __host__ __device__ inline int box_rows(int i) { return i < 5 ? 1 << i : (i - 4) * 32; }
 
-// Tiles along an expert's rows, and the rows of each (cut evenly, a multiple of 16).
+// Tiles along an expert's rows (cut evenly, a multiple of 16 each).
 __device__ __forceinline__ int m_tiles_of(int m) { return ceil_div(m, kTileRows); }
 
 // ------------------------------------------------------------------ plan
@@ -253,39 +255,68 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *
 // these as outputs.
 __device__ __forceinline__ float silu_mul(float z, float up) { return __fdividef(z, 1.f + __expf(-z)) * up; }
 
-// Outputs of one thread: weight row n, rows row0 .. row0 + cnt - 1 of X, sums v.  With SiLU*mul the up value
-// of gate row n comes from the thread of row n + 8 (lane ^ 8); every lane of the warp calls this alike.
+// Where outputs go: the launch's parameters, which the epilogue keeps in registers (read in its loop, they are
+// fetched from constant memory again and again between the tcgen05 and barrier instructions, and miss).
+template <typename T> struct Out {
+    T *Y;
+    long long stride;
+    const float *row_scale;
+    int N;
+    bool silu;
+};
+
+// The scales of a chunk's rows, lane i that of row i (i + 16 too).
+template <typename T> __device__ __forceinline__ float scales_of(const Out<T> &o, int row0, int cnt) {
+    const int i = threadIdx.x & 15;
+    return o.row_scale && i < cnt ? o.row_scale[row0 + i] : 1.f;
+}
+
+// Outputs of one thread: weight row n, rows row0 .. row0 + cnt - 1 of X (up to 16), sums v; scale from scales_of().
+// A warp writes 64 bytes to a row (32 with SiLU*mul), and no branch is taken row by row: with one at every row a
+// chunk of 16 rows took 2100 to 3700 clocks instead of 850.  With SiLU*mul lanes of gate rows finish rows 0 .. 7 and lanes of up
+// rows 8 .. 15: each sends its partner (lane ^ 8) the eight sums that one needs.  Every lane of the warp calls this
+// alike.
 template <typename T>
-__device__ __forceinline__ void emit_rows(const ExpertParams &p, int n, int row0, int cnt, const float (&v)[16]) {
-    T *Y = reinterpret_cast<T *>(p.Y);
-    const int col = p.silu ? ((n >> 4) << 3) + (n & 7) : n;
-    const bool writer = n < p.N && !(p.silu && (n & 8));
-    T *y = Y + (long long)row0 * p.y_stride + col;
-    float s[16];
+__device__ __forceinline__ void emit_rows(const Out<T> &o, int n, int row0, int cnt, const float (&v)[16], float scale) {
+    if (o.silu) {                                       // (N is a multiple of 16: a gate row in range has its up row)
+        const bool up_lane = n & 8;
+        const int first = up_lane ? 8 : 0;
+        T *y = o.Y + (long long)(row0 + first) * o.stride + ((n >> 4) << 3) + (n & 7);
+        const int mine = n < o.N ? cnt - first : 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = (p.row_scale && i < cnt) ? p.row_scale[row0 + i] : 1.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if (i >= cnt) break;                            // uniform across the warp
-        float x = v[i];
-        if (p.silu) {
-            const float up = __shfl_xor_sync(0xffffffffu, x, 8);
-            x = silu_mul(x, up);
+        for (int i = 0; i < 8; ++i, y += o.stride) {
+            const float got = __shfl_xor_sync(0xffffffffu, up_lane ? v[i] : v[i + 8], 8);
+            const float gate = up_lane ? got : v[i], up = up_lane ? v[i + 8] : got;
+            const float s = __shfl_sync(0xffffffffu, scale, first + i);
+            const T out = from_f32<T>(silu_mul(gate, up) * s);
+            if (i < mine) *y = out;
         }
-        if (writer) y[i * p.y_stride] = from_f32<T>(x * s[i]);
+    } else {
+        T *y = o.Y + (long long)row0 * o.stride + n;
+        const int mine = n < o.N ? cnt : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i, y += o.stride) {
+            const T out = from_f32<T>(v[i] * __shfl_sync(0xffffffffu, scale, i));
+            if (i < mine) *y = out;
+        }
     }
+}
+
+__device__ __forceinline__ void ld_cg_rows4(const float *p, float *v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = ld_cg_f32(p + k * kTileN);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_constant__ ExpertParams p) {
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], accf_bar[2], acce_bar[2], drain_bar;
-    __shared__ int unit_meta[kUnitRing][4];             // {unit (-1: no more), MMA N, K boxes}, by the producer
-    __shared__ int acc_unit[2];                         // unit of an accumulator (-1: no more), by the MMA thread
+    __shared__ Unit units[kUnitRing];                   // what the stages hold (expert -1: no more), by the producer
+    __shared__ int acc_unit[2];                         // place there of an accumulator's (-1: no more), by the MMA thread
     __shared__ int unit0[kMaxExperts];
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
-    __shared__ int last_flag[kEpiSets];
+    __shared__ int last_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     int *const status = g_experts_status;
@@ -297,7 +328,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf_bar[b], 2);                 // tcgen05.commit and the MMA thread's unit number
-            mbar_init(&acce_bar[b], 4);
+            mbar_init(&acce_bar[b], kEpiSets * 4);
         }
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
@@ -344,9 +375,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
                 const int box = box_of(t.rows);
                 const CUtensorMap *const tmX = &p.tmX[box];
                 const uint32_t box_bytes = (uint32_t)(kBoxW + box_rows(box) * kBK * 2);
-                unit_meta[slot][0] = u;
-                unit_meta[slot][1] = t.mrows;
-                unit_meta[slot][2] = t.k1 - t.k0;
+                units[slot] = t;
                 if (++slot == kUnitRing) slot = 0;
                 int next = n_units;
                 bool claimed = false;
@@ -377,7 +406,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
             // every copy has landed before the CTA ends
             drain_issued(full_bar, kStages, issued, kExWaitNs, status);
             if (!aborted && mbar_wait_bounded(&empty_bar[s], ph ^ 1, &abort_flag, kExWaitNs, status, -1, kSiteEmpty)) {
-                unit_meta[slot][0] = -1;
+                units[slot].expert = -1;
                 mbar_arrive(&full_bar[s]);
             }
         }
@@ -392,22 +421,16 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
             const uint64_t desc0 = sw128_desc(ring_u);
             while (ok) {
                 if (!mbar_wait_bounded(&full_bar[s], ph, &abort_flag, kExWaitNs, status, -1, kSiteFull)) break;
-                const int unit = unit_meta[slot][0], mrows = unit_meta[slot][1];
-                int left = unit_meta[slot][2];
+                const int here = slot, mrows = units[slot].mrows;
+                const bool more = units[slot].expert >= 0;
+                int left = units[slot].k1 - units[slot].k0;
                 if (++slot == kUnitRing) slot = 0;
                 const int buf = (int)(acc_i & 1u);
                 if (!mbar_wait_bounded(&acce_bar[buf], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc)) break;
-                if (unit < 0) {
-                    // the end goes to both epilogue sets, the other one's accumulator included
+                if (!more) {
                     acc_unit[buf] = -1;
                     mbar_arrive(&accf_bar[buf]);
                     mbar_arrive(&accf_bar[buf]);
-                    ++acc_i;
-                    const int other = (int)(acc_i & 1u);
-                    if (!mbar_wait_bounded(&acce_bar[other], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc)) break;
-                    acc_unit[other] = -1;
-                    mbar_arrive(&accf_bar[other]);
-                    mbar_arrive(&accf_bar[other]);
                     break;
                 }
                 const uint32_t idesc = p.idesc | ((uint32_t)(mrows >> 3) << 17);
@@ -442,7 +465,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
                     tc_fence_after();
                 }
                 if (!ok) break;
-                acc_unit[buf] = unit;
+                acc_unit[buf] = here;
                 mbar_arrive(&accf_bar[buf]);
                 tc_commit(&accf_bar[buf]);
                 ++acc_i;
@@ -454,59 +477,78 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        // Two sets of four warps, one for each accumulator.
+        // Two sets of four warps, each with every other 16 rows of a tile.
         const int set = (warp - 2) >> 2;
         const int q = warp & 3;                         // TMEM lane quadrant this warp may read
         const int row = q * 32 + lane;                  // weight row within the tile
-        const bool leader = (threadIdx.x - 64) == (unsigned)(set * 128);
-        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(set * kTileRows);
+        const bool leader = threadIdx.x == 64;
+        constexpr int kStep = kEpiSets * 16;
+        const Out<T> out = {static_cast<T *>(p.Y), p.y_stride, p.row_scale, p.N, p.silu != 0};
+        float *const parts = p.part;
         for (uint32_t i = 0;; ++i) {
-            const bool ab = !mbar_wait_bounded(&accf_bar[set], i & 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc);
-            const int u = ab ? -1 : acc_unit[set];
-            if (vote_or(u < 0, 1 + set, 128)) break;    // the four warps stop together
+            const int buf = (int)(i & 1u);
+            const bool ab = !mbar_wait_bounded(&accf_bar[buf], (i >> 1) & 1u, &abort_flag, kExWaitNs, status, -1, kSiteAcc);
+            const int u = ab ? -1 : acc_unit[buf];
+            if (vote_or(u < 0, 1, kEpiSets * 128)) break;   // the eight warps stop together
             tc_fence_after();
-            const Unit t = unit_at(p, unit0, head, u);
-            float *part = p.part + ((size_t)t.part + (size_t)t.j * (t.mrows / 16)) * (16 * kTileN) + row;
+            const Unit t = units[u];
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kTileRows);
+            float *part = parts + ((size_t)t.part + (size_t)t.j * (t.mrows / 16)) * (16 * kTileN) + row;
+            uint32_t r[16], ahead[16];
+            if (set * 16 < t.rows) tmem_ld16(taddr + (uint32_t)(set * 16), ahead);
 #pragma unroll 1
-            for (int c = 0; c < t.rows; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(taddr + (uint32_t)c, r);
-                tmem_ld_wait16(r);
+            for (int c = set * 16; c < t.rows; c += kStep) {
+                const int cnt = min(16, t.rows - c);
+                const float scale = t.nu == 1 ? scales_of(out, t.row0 + c, cnt) : 1.f;
+                tmem_ld_wait16(ahead);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) r[k] = ahead[k];
+                if (c + kStep < t.rows) tmem_ld16(taddr + (uint32_t)(c + kStep), ahead);    // under this chunk's work
                 float v[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
                 if (t.nu == 1) {
-                    emit_rows<T>(p, t.n0 + row, t.row0 + c, min(16, t.rows - c), v);
+                    emit_rows(out, t.n0 + row, t.row0 + c, cnt, v, scale);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        if (c + k < t.rows) part[(size_t)(c + k) * kTileN] = v[k];
+                        if (k < cnt) part[(size_t)(c + k) * kTileN] = v[k];
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acce_bar[set]);
+            if (lane == 0) mbar_arrive(&acce_bar[buf]);
             if (t.nu == 1) continue;
             // the tile's last unit to arrive adds all partials, in K order
-            named_bar_sync(3 + set, 128);
-            if (leader) last_flag[set] = atom_add_acqrel_gpu(&p.tile_cnt[t.split], 1u) == (unsigned int)(t.nu - 1) ? 1 : 0;
-            named_bar_sync(3 + set, 128);
-            if (!last_flag[set]) continue;
-            const float *from = p.part + (size_t)t.part * (16 * kTileN) + row;
+            named_bar_sync(2, kEpiSets * 128);
+            if (leader) last_flag = atom_add_acqrel_gpu(&p.tile_cnt[t.split], 1u) == (unsigned int)(t.nu - 1) ? 1 : 0;
+            named_bar_sync(2, kEpiSets * 128);
+            if (!last_flag) continue;
+            const float *from = parts + (size_t)t.part * (16 * kTileN) + row;
             const size_t step = (size_t)(t.mrows / 16) * (16 * kTileN);
 #pragma unroll 1
-            for (int c = 0; c < t.rows; c += 16) {
+            for (int c = set * 16; c < t.rows; c += kStep) {
+                const int cnt = min(16, t.rows - c);
+                const float scale = scales_of(out, t.row0 + c, cnt);
                 float v[16];
+                const float *f = from + (size_t)c * kTileN;
+                for (int j = 0; j < t.nu; j += 2, f += 2 * step) {
+                    // rows by fours, those past the tile's whatever the block of 16 holds: nobody reads their sums
+                    float w[2][16];
+                    const bool two = j + 1 < t.nu;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = 0.f;
-                for (int j = 0; j < t.nu; ++j) {
-                    float w[16];
+                    for (int k = 0; k < 16; k += 4)
+                        if (k < cnt) {
+                            ld_cg_rows4(f + k * kTileN, w[0] + k);
+                            if (two) ld_cg_rows4(f + step + k * kTileN, w[1] + k);
+                        }
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) w[k] = c + k < t.rows ? ld_cg_f32(from + j * step + (size_t)(c + k) * kTileN) : 0.f;
+                    for (int k = 0; k < 16; ++k) v[k] = j == 0 ? w[0][k] : v[k] + w[0][k];
+                    if (two)
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = j == 0 ? w[k] : v[k] + w[k];
+                        for (int k = 0; k < 16; ++k) v[k] += w[1][k];
                 }
-                emit_rows<T>(p, t.n0 + row, t.row0 + c, min(16, t.rows - c), v);
+                emit_rows(out, t.n0 + row, t.row0 + c, cnt, v, scale);
             }
         }
     }
