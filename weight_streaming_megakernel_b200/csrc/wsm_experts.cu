@@ -30,7 +30,8 @@ static __device__ int g_experts_status[kOpStatusInts];
 
 constexpr int kMaxExperts = 1024;
 constexpr int kTileN = 128;         // weight rows per tile (MMA M)
-constexpr int kTileRows = 256;      // most rows of X per tile (MMA N)
+constexpr int kTileRowsLog = 8;
+constexpr int kTileRows = 1 << kTileRowsLog;    // most rows of X per tile (MMA N)
 constexpr int kBK = 64;             // K elements per box (a 128-byte swizzle row)
 constexpr int kStageBytes = 48 * 1024;
 constexpr int kStages = 4;
@@ -55,8 +56,8 @@ struct ExpertRec {
     int nu, ku;                     // units of each split tile, K boxes of a unit
     int mrows;                      // rows per tile, a multiple of 16
 };
-// Head of the scratch: [0] units, [1] tiles before the split ones, [2] claim counter.
-enum : int { kHdrUnits = 0, kHdrHead = 1, kHdrClaim = 2 };
+// Head of the scratch: [0] units, [1] tiles before the split ones, [2] claim counter, [3] log2 of a tile's most rows.
+enum : int { kHdrUnits = 0, kHdrHead = 1, kHdrClaim = 2, kHdrRowsLog = 3 };
 constexpr int kHdrBytes = 256;
 
 struct ExpertParams {
@@ -94,7 +95,7 @@ __host__ __device__ inline int box_of(int rows) {
 __host__ __device__ inline int box_rows(int i) { return i < 5 ? 1 << i : (i - 4) * 32; }
 
 // Tiles along an expert's rows (cut evenly, a multiple of 16 each).
-__device__ __forceinline__ int m_tiles_of(int m) { return ceil_div(m, kTileRows); }
+__device__ __forceinline__ int m_tiles_of(int m, int rows_log) { return (m + (1 << rows_log) - 1) >> rows_log; }
 
 // ------------------------------------------------------------------ plan
 
@@ -135,17 +136,27 @@ __global__ void __launch_bounds__(kMaxExperts) experts_plan_kernel(const __grid_
     }
     if (have && (raw != hi || (e == 0 && raw0 != lo0))) record_op_error(g_experts_status, kCodeInvalid, e, kSiteOffsets);
     const int m = have ? hi - lo : 0;
-    const int mt = m_tiles_of(m);
-    const int tiles = mt * p.n_g;
-    const int tile_end = block_scan<false>(tiles, warp_tot);
-    if (e == (int)blockDim.x - 1) tiles_all = tile_end;
-    __syncthreads();
-    const int total = tiles_all;
-    // Few tiles: all are cut so that each SM gets about three units.  Many: whole tiles, and the last one per
-    // SM cut in two, so that the SMs end together.  A unit is long against its partial sums' way out and back.
+    // The highest tiles read the least (for 256 rows of X 48 KB to a K box, for 64 24 KB), but a call with few of them
+    // leaves SMs without: below one to three SMs, lower ones.  (On a B200, 400 rows of 4 experts of 1152 x 3944: 38 us
+    // in tiles of up to 256 rows, 26 of 128; 1652 of 15 experts of 304 x 904: 17.5 and 15.4; 300 rows of one expert of
+    // 4096 x 4096, 64 tiles, stay with 256: 29 us, 33 in tiles of 128.)
+    int rows_log = kTileRowsLog, mt, tiles, tile_end, total;
+    for (;; --rows_log) {
+        mt = m_tiles_of(m, rows_log);
+        tiles = mt * p.n_g;
+        tile_end = block_scan<false>(tiles, warp_tot);
+        if (e == (int)blockDim.x - 1) tiles_all = tile_end;
+        __syncthreads();
+        total = tiles_all;
+        if (total >= p.sms / 3 || (1 << rows_log) <= kNarrow) break;
+        __syncthreads();
+    }
+    // Many tiles: whole ones, and the last one per SM cut in two, so that the SMs end together.  Few: cut so that each
+    // SM gets about three units of few rows, one of more (a partial sum's way out and back costs rows; 48 rows of one
+    // expert of 4096 x 4096: 24 us with three units to an SM, 18 with one).  A unit is long against that.
     const int head = total >= 3 * p.sms ? total - p.sms : 0;
-    const int want = total >= 3 * p.sms ? 2 : ceil_div(3 * p.sms, max(total, 1));
     const int mrows = mt > 0 ? ceil_div(ceil_div(m, mt), 16) * 16 : 16;
+    const int want = total >= 3 * p.sms ? 2 : mrows <= 32 ? ceil_div(3 * p.sms, max(total, 1)) : p.sms / max(total, 1);
     const int least = mrows <= 64 ? 8 : mrows <= 128 ? 16 : 32;
     int nu = max(1, min(want, p.kb / least));
     const int whole = min(max(head - (tile_end - tiles), 0), tiles);   // tiles of this expert that stay whole
@@ -175,6 +186,7 @@ __global__ void __launch_bounds__(kMaxExperts) experts_plan_kernel(const __grid_
         p.hdr[kHdrUnits] = unit_end;
         p.hdr[kHdrHead] = head;
         p.hdr[kHdrClaim] = 0;
+        p.hdr[kHdrRowsLog] = rows_log;
     }
 }
 
@@ -193,7 +205,7 @@ struct Unit {
 
 // (unit0 of the experts in shared memory: the last expert whose first unit is not past u has it -- experts
 // without rows share their successor's unit0 and come before it)
-__device__ __forceinline__ Unit unit_at(const ExpertParams &p, const int *unit0, int head, int u) {
+__device__ __forceinline__ Unit unit_at(const ExpertParams &p, const int *unit0, int head, int rows_log, int u) {
     int lo = 0, hi = p.experts - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -202,7 +214,7 @@ __device__ __forceinline__ Unit unit_at(const ExpertParams &p, const int *unit0,
     }
     const ExpertRec r = p.rec[lo];
     const int v = u - r.unit0;
-    const int mt = m_tiles_of(r.m);
+    const int mt = m_tiles_of(r.m, rows_log);
     const int whole = min(max(head - r.tile0, 0), mt * p.n_g);
     Unit t;
     t.expert = lo;
@@ -343,7 +355,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
-    const int n_units = p.hdr[kHdrUnits], head = p.hdr[kHdrHead];
+    const int n_units = p.hdr[kHdrUnits], head = p.hdr[kHdrHead], rows_log = p.hdr[kHdrRowsLog];
     const uint32_t ring_u = smem_u32(ring);
 
     if (warp == 0) {
@@ -366,10 +378,10 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
             }
             int u = (int)blockIdx.x;
             while (!aborted && u < n_units) {
-                const Unit t = unit_at(p, unit0, head, u);
+                const Unit t = unit_at(p, unit0, head, rows_log, u);
                 const int step = t.mrows <= kNarrow ? 2 : 1;
                 // weights with one reader leave L2 first
-                const uint64_t pol_w = p.rec[t.expert].m <= kTileRows ? pol_once : pol_keep;
+                const uint64_t pol_w = p.rec[t.expert].m <= 1 << rows_log ? pol_once : pol_keep;
                 // rows past the box in the MMA's N are what the stage held before, rows in it past the tile's another
                 // expert's: nobody reads their sums
                 const int box = box_of(t.rows);
