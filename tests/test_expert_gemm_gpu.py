@@ -70,6 +70,20 @@ def test_cut_along_k(dtype):
     run_and_check(*make([300, 7], 256, 4096, dtype, seed=3), silu=True)
 
 
+@pytest.mark.parametrize("m", [64, 65, 80, 127, 129, 176, 240, 241, 255, 256, 257, 300])
+def test_row_counts_of_high_tiles(m):
+    """Enough tiles for the highest ones: up to 256 rows each."""
+    run_and_check(*make([3, m, 0, 1], 6300, 72, seed=m), scaled=m % 2 == 0)
+    run_and_check(*make([0, m], 6304, 200, torch.float16, seed=m), silu=True, scaled=m % 2 == 1)
+
+
+def test_high_tiles_cut_along_k():
+    """A tile of up to 256 rows whose units are joined; and one of 128 rows, and of 64."""
+    run_and_check(*make([200], 6300, 4104, seed=1), scaled=True)
+    run_and_check(*make([5, 100], 3200, 4104, seed=2), silu=True, scaled=True)
+    run_and_check(*make([190], 640, 4104, torch.float16, seed=3), silu=True)
+
+
 @pytest.mark.parametrize("counts", [[0] * 40 + [1], [1] + [0] * 40, [0] * 8, [5] * 33, [0, 700, 0, 0, 3],
                                     [i % 3 for i in range(1024)]])
 def test_ragged(counts):
