@@ -129,6 +129,25 @@ def test_padding_and_bad_tokens():
     assert not got.logprob.any()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab", [9, 1003, 9001])
+def test_many_rows(dtype, vocab):
+    """More rows than the GPU takes at once, hard ones among them."""
+    x, t = make(900, vocab, dtype, seed=vocab)
+    x[::50] = 1.0                                       # all alike
+    x[1::50] = -math.inf                                # nothing left
+    x[2::50, vocab // 3:] = -math.inf
+    x[3::50] = torch.arange(vocab).to(dtype)            # rising
+    x[4::50, vocab // 2:] = torch.finfo(dtype).min
+    x[5::50, vocab // 2] = math.nan
+    t[6::50] = -1
+    for top in sorted({0, min(3, vocab), min(32, vocab)}):
+        run_and_check(x, t, top, f"top {top}")
+    wide = torch.full((900, vocab + 5), math.nan, dtype=dtype, device=DEV)
+    wide[:, 3:3 + vocab] = x
+    run_and_check(wide[:, 3:3 + vocab], t, min(3, vocab), "a wider buffer")
+
+
 def test_strides_and_alignment():
     """Rows of a wider buffer, at every distance from a 16-byte boundary."""
     for dtype in (torch.float32, torch.bfloat16):

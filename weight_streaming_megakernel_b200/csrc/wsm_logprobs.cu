@@ -29,7 +29,12 @@ static __device__ int g_logprobs_status[kOpStatusInts];
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;         // one alternative per lane of a warp's list
-constexpr int kLpLoads = 8;         // 16-byte loads of a thread in a turn over the row
+// 16-byte loads of a thread in a turn over the row.  Where every SM has a block or two, many loads to each; with more
+// rows fewer, for three blocks to an SM: what follows a row's pass (its alternatives, some 3 us) hides behind the
+// others' passes.  (On a B200, 8 loads and two blocks, 4 and three: 128 rows of 128000 bf16, nine in ten masked, 17 and 20 us, 148
+// rows of 128000 without alternatives 14.2 and 16.0; 391 rows of 102912 with 32 alternatives 51 and 39, 707 of 3405
+// with 5 20 and 14, 412 of 34409 fp16 25 and 16.)
+constexpr int kFewRowsLoads = 8, kManyRowsLoads = 4;
 constexpr int kLpUnroll = 4;        // ... and how many of them it unpacks at a time
 constexpr int kFound = 512;         // elements that reach the floor there is room for
 constexpr int kMaxCluster = 8;      // the portable cluster size
@@ -159,7 +164,7 @@ template <> struct Vec16<__half> {
 
 // Where a block's part of a row lies: elements before the first 16-byte boundary (the first block's), whole
 // vectors (dealt to the row's blocks in consecutive stretches), and the rest (the last block's).
-template <typename T> struct RowPart {
+template <typename T, int kLpLoads> struct RowPart {
     static constexpr int VEC = 16 / (int)sizeof(T);
     static constexpr int kStep = kLpThreads * kLpLoads; // vectors a block takes per turn
     const T *x;
@@ -195,10 +200,10 @@ __device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b <
 
 // The best p.top of a block's part by sorted lists: every element is offered to its warp's.  Leaves them in
 // best[], best first.  All threads.
-template <typename T>
-__device__ __noinline__ void top_by_lists(const RowPart<T> &r, int k, unsigned long long (*warp_top)[kMaxTop],
+template <typename T, int kLpLoads>
+__device__ __noinline__ void top_by_lists(const RowPart<T, kLpLoads> &r, int k, unsigned long long (*warp_top)[kMaxTop],
                                           unsigned long long *best) {
-    constexpr int VEC = RowPart<T>::VEC;
+    constexpr int VEC = RowPart<T, kLpLoads>::VEC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     TopList top;
     top.key = 0ull;
@@ -240,9 +245,9 @@ __device__ __noinline__ void top_by_lists(const RowPart<T> &r, int k, unsigned l
     __syncthreads();
 }
 
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
-    constexpr int VEC = RowPart<T>::VEC;
+template <typename T, bool kTop, int kLpLoads>
+__global__ void __launch_bounds__(kLpThreads, kLpLoads == kFewRowsLoads ? 2 : 3) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+    constexpr int VEC = RowPart<T, kLpLoads>::VEC;
     constexpr int NB = kLpUnroll * VEC;                 // elements of a thread's block
     __shared__ int warp_tops[kLpWarps];
     __shared__ float2 warp_sums[kLpWarps];
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     if (p.ctas > 1) cluster_sync_all();                 // every block of the row is there to be written to
     pdl_wait();
     pdl_launch_dependents();
-    const RowPart<T> r(p, row, part);
+    const RowPart<T, kLpLoads> r(p, row, part);
     // the token asked for and its logit: two loads in a row, well before they are needed
     long long token = -1;
     float token_x = 0.f;
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
             __syncthreads();
         } else {
             // (the found elements' memory holds the lists now)
-            top_by_lists<T>(r, p.top, reinterpret_cast<unsigned long long(*)[kMaxTop]>(found), best);
+            top_by_lists<T, kLpLoads>(r, p.top, reinterpret_cast<unsigned long long(*)[kMaxTop]>(found), best);
         }
         if (p.ctas > 1 && threadIdx.x < kMaxTop) {
             const uint32_t a = map_to_rank(smem_u32(&all_top[part][threadIdx.x]), 0);
@@ -509,11 +514,15 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
     }
 }
 
-template <typename T>
-wsm_status run_logprobs(const LogprobsParams &p, cudaStream_t stream) {
-    const dim3 grid((unsigned)((long long)p.rows * p.ctas));
-    return p.top > 0 ? op_launch(&logprobs_kernel<T, true>, grid, kLpThreads, 0, stream, p, p.ctas)
-                     : op_launch(&logprobs_kernel<T, false>, grid, kLpThreads, 0, stream, p, p.ctas);
+template <typename T, bool kTop>
+wsm_status run_logprobs(const LogprobsParams &p, int sms, cudaStream_t stream) {
+    const long long blocks = (long long)p.rows * p.ctas;
+    const dim3 grid((unsigned)blocks);
+    return blocks <= 2ll * sms ? op_launch(&logprobs_kernel<T, kTop, kFewRowsLoads>, grid, kLpThreads, 0, stream, p, p.ctas)
+                               : op_launch(&logprobs_kernel<T, kTop, kManyRowsLoads>, grid, kLpThreads, 0, stream, p, p.ctas);
+}
+template <typename T> wsm_status run_logprobs(const LogprobsParams &p, int sms, cudaStream_t stream) {
+    return p.top > 0 ? run_logprobs<T, true>(p, sms, stream) : run_logprobs<T, false>(p, sms, stream);
 }
 
 }  // namespace
@@ -564,6 +573,6 @@ extern "C" wsm_status wsm_token_logprobs(const wsm_logprobs *a, wsm_stream_t str
     while (p.ctas < kMaxCluster && (long long)p.rows * p.ctas * 2 <= 2ll * sms && (size_t)p.vocab * es / (2 * p.ctas) >= 4096)
         p.ctas *= 2;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    if (a->dtype == WSM_DTYPE_FP32) return run_logprobs<float>(p, stream);
-    return a->dtype == WSM_DTYPE_BF16 ? run_logprobs<__nv_bfloat16>(p, stream) : run_logprobs<__half>(p, stream);
+    if (a->dtype == WSM_DTYPE_FP32) return run_logprobs<float>(p, sms, stream);
+    return a->dtype == WSM_DTYPE_BF16 ? run_logprobs<__nv_bfloat16>(p, sms, stream) : run_logprobs<__half>(p, sms, stream);
 }
