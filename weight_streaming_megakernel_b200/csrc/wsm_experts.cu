@@ -17,6 +17,13 @@
 //   accumulators in tensor memory, warps 2-9 take finished ones out: activation, scale, rounding, stores.  A
 //   tile cut along K leaves fp32 partials, which its last unit to finish adds in K order, so results do not
 //   depend on which SM ran what.
+//
+// Measured on a B200 (floors: weights at the 6440 GB/s of a copy, products at cuBLAS' 1.67 PFLOP/s): 16 rows over 32
+// experts of 4096 x 4096, 68.6 us (66: the weights come at 5.6 to 6.2 TB/s, the tensor pipe is 4 % busy); 1000 rows over
+// 64 experts of 4096 x 1280, 102 us (106 were all experts to get rows); 8192 rows over 16 experts of 6144 x 4096, 435 to
+// 485 us by the clock that the power leaves (246, and 296 at cuBLAS' sustained rate): 48 KB to a K box out of L2 into
+// each SM and about 562 clocks to a stage, against 512 of the products alone.  CTA pairs, which halve what W costs L2,
+// took 429 to 490 us there, and 75 and 120 us in the first two, as half as many tiles are in flight.
 #include "wsm_ops.cuh"
 #include "wsm_tcgen05.cuh"
 
