@@ -252,6 +252,13 @@ __device__ __forceinline__ Unit unit_at(const ExpertParams &p, const int *unit0,
     return t;
 }
 
+// True in one lane of the warp, which all lanes reach together.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0u;
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z,
                                             uint64_t policy) {
     asm volatile(
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_normal();
             int s = 0, slot = 0;
             uint32_t ph = 0;
@@ -432,8 +439,8 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // One thread, and a stage's MMAs take as little as 128 clocks: nothing in the loop over a unit's stages but
-        // the wait, the instructions and the commit.
-        if (lane == 0) {
+        // the wait, the instructions and the commit.  Its thread is elected, not lane 0: @E
+        if (elect_one()) {
             int s = 0, slot = 0;
             uint32_t ph = 0, acc_i = 0;
             bool ok = true;
