@@ -18,12 +18,14 @@
 //   tile cut along K leaves fp32 partials, which its last unit to finish adds in K order, so results do not
 //   depend on which SM ran what.
 //
-// Measured on a B200 (floors: weights at the 6440 GB/s of a copy, products at cuBLAS' 1.67 PFLOP/s): 16 rows over 32
-// experts of 4096 x 4096, 68.6 us (66: the weights come at 5.6 to 6.2 TB/s, the tensor pipe is 4 % busy); 1000 rows over
-// 64 experts of 4096 x 1280, 102 us (106 were all experts to get rows); 8192 rows over 16 experts of 6144 x 4096, 435 to
-// 485 us by the clock that the power leaves (246, and 296 at cuBLAS' sustained rate): 48 KB to a K box out of L2 into
-// each SM and about 562 clocks to a stage, against 512 of the products alone.  CTA pairs, which halve what W costs L2,
-// took 429 to 490 us there, and 75 and 120 us in the first two, as half as many tiles are in flight.
+// Measured on a B200 (floors: weights at the 6440 GB/s of a copy, products at cuBLAS' 1.67 PFLOP/s, 1.39 sustained): 16
+// rows over 32 experts of 4096 x 4096, 65 to 71 us by which experts get them (66: weights at 5.6 to 6.2 TB/s, the
+// tensor pipe 4 % busy); 1000 rows over 64 experts of 4096 x 1280, 101 to 109 us (106 were all to get rows); 8192 rows
+// over 16 experts of 6144 x 4096, 395 us in a burst and 455 in a loop, where the power leaves 1.3 to 1.4 GHz (246,
+// 296).  There some 43 KB a stage come out of L2 at 60 bytes a clock, about what an SM takes in: 550 thousand clocks,
+// as many without the products, and 370 without the copies.  CTA pairs (cta_group::2) load 30 % less and took 8 %
+// less time there, but as much or 4 % more at 3000 to 8192 rows over smaller experts and 117 to 128 us on the 1000
+// rows: half as many tiles are in flight.
 #include "wsm_ops.cuh"
 #include "wsm_tcgen05.cuh"
 
@@ -439,7 +441,9 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         // One thread, and a stage's MMAs take as little as 128 clocks: nothing in the loop over a unit's stages but
-        // the wait, the instructions and the commit.  Its thread is elected, not lane 0: @E
+        // the wait, the instructions and the commit. The thread is elected, not lane 0:
+        // in a branch on the lane the compiler cannot tell that only one runs, and the thread spends 111 clocks on each
+        // tcgen05.mma, 54 so.
         if (elect_one()) {
             int s = 0, slot = 0;
             uint32_t ph = 0, acc_i = 0;
