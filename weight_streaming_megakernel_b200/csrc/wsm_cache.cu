@@ -126,12 +126,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // do not depend on timing.
 //
 // Measured on a B200 (floor: the cache's bytes at the 6440 GB/s of a copy): one token over 131041 of a 16-bit cache of
-// 8 heads of 128 105 us (floor 83); 64 ragged sequences of up to 4000 tokens 36 to 41 us (22); 96 over an 8-bit cache
-// 56 to 62 us (34): the warps issue in 54 % of the cycles and the cache comes at 4.2 TB/s; one sequence of 37 tokens
+// 8 heads of 128 102 to 106 us (floor 83); 64 ragged sequences of up to 4000 tokens 36 to 42 us (22); 96 over an 8-bit cache
+// 56 to 60 us (34): the warps issue in 54 % of the cycles and the cache comes at 4.2 TB/s; one sequence of 37 tokens
 // 7.0 us.  About 4.5 us of each is the chain of reads that finds a warp its first tokens (lengths, then the table, then
-// keys), 6 to 7 the join's, launched under the main kernel but for its reads.  With the arithmetic taken out the three
-// large ones took 98, 39 and 54 us: what is left lies in the load path and these fixed costs.  A join by the last
-// block to arrive instead of a second launch: the same on ragged and long batches, 71 us on the 8-bit one, whose
+// keys), 5 to 6 the join's, which finds its items' places while the main kernel runs.  With the arithmetic taken out
+// the three large ones took 98, 39 and 54 us: what is left lies in the load path and these fixed costs.  A join by the
+// last block to arrive instead of a second launch: the same on ragged and long batches, 71 us on the 8-bit one, whose
 // registers it took.
 
 constexpr int kGroup = 16;          // tokens a warp takes at a time (the MMA's k)
@@ -155,7 +155,6 @@ struct AttnParams {
     const int *table, *lengths;
     float *part_o;                  // [workers][2][16][D]
     float2 *part_ml;                // [workers][2][16]: reference (base 2) and sum
-    int *prefix;                    // [batch + 1] copy for the join
     long long q_row, q_head, o_row, o_head;        // elements
     long long k_page, k_tok, k_head, v_page, v_tok, v_head;
     long long table_stride;
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    // ---- prefix sums of the sequences' groups (each block its own copy; block 0's goes to the join)
+    // ---- prefix sums of the sequences' groups (each block its own copy)
     int carry = 0;
     for (int b0 = 0; b0 < p.batch; b0 += NW * 32) {
         const int b = b0 + (int)threadIdx.x;
@@ -332,8 +331,6 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         if (b == 0) prefix[0] = 0;
         __syncthreads();
     }
-    if (p.prefix && blockIdx.x == 0)
-        for (int b = threadIdx.x; b <= p.batch; b += NW * 32) p.prefix[b] = prefix[b];
 
     // ---- this warp's range; neighbouring ranges lie on different SMs, so a short call's few spread over the GPU
     const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
@@ -740,22 +737,40 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
 // Join the partials of the items that were cut: block (item, rows).  Each row's partials are dealt to as many
 // warps as there are for it (p.join_split), which take every join_split-th in range order, kJoinUnroll at a time;
 // the warps' sums are added in warp order: the same result every time.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 16;      // at most
 constexpr int kJoinUnroll = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float4 sum[kJoinWarps][D / 4];
     __shared__ float2 ml[kJoinWarps];
+    __shared__ int2 groups[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hq = p.kv_heads * p.q_tiles;
     const int b = (int)blockIdx.x / hq, item = (int)blockIdx.x - b * hq;
     const int h = p.q_tiles == 1 ? item : item / p.q_tiles, qt = item - h * p.q_tiles;
     const int rows = min(16, p.group - qt * 16);
-    pdl_wait();
+    // Where the item lies in the line, while the main kernel runs: its blocks let this one begin after their own wait
+    // for what came before, so the lengths are there.
+    int before = 0, all = 0;
+    for (int i = threadIdx.x; i < p.batch; i += (int)blockDim.x) {
+        const int g = span_of(p, p.lengths[i]).groups;
+        all += g;
+        before += i < b ? g : 0;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) groups[warp] = make_int2(before, all);
+    __syncthreads();
+    before = all = 0;
+    for (int w = 0; w < (int)blockDim.x >> 5; ++w) {
+        before += groups[w].x;
+        all += groups[w].y;
+    }
+    const int n = span_of(p, p.lengths[b]).groups;
+    const int at = (before + kItemCost * b) * hq + item * (n + kItemCost);
+    const int per = share_of((all + kItemCost * p.batch) * hq, p.workers);
+    pdl_wait();                                         // (before any return: who comes next waits for this kernel alone)
     pdl_launch_dependents();
-    const int *prefix = p.prefix;
-    const int n = prefix[b + 1] - prefix[b], at = line_of(prefix, hq, b) + item * (n + kItemCost);
-    const int per = share_of(line_of(prefix, hq, p.batch), p.workers);
     if (n <= kSnapGroups) return;                       // never cut
     // group g lies kItemCost + g past the item's place in the line; the ranges of the first and the last one
     const int w0 = (at + kItemCost) / per, w1 = (at + kItemCost + n - 1) / per;
@@ -888,7 +903,7 @@ wsm_status run_attention(const AttnParams &p, int dev, int sms, cudaStream_t str
     if ((st = op_launch(&attention_kernel<T, kE4m3, D>, dim3((unsigned)sms), Geo::kWarps * 32, smem, stream, p)) != WSM_OK)
         return st;
     if (!join) return WSM_OK;
-    return op_launch(&attention_join_kernel<T, D>, join_grid, kJoinWarps * 32, 0, stream, p);
+    return op_launch(&attention_join_kernel<T, D>, join_grid, p.rows_per_cta * p.join_split * 32, 0, stream, p);
 }
 
 int attention_warps(int head_dim, bool e4m3) {
@@ -906,10 +921,10 @@ bool attention_may_cut(long long max_tokens, int window) {
     return (span + kGroup - 1) / kGroup > kSnapGroups;
 }
 
-// Partials of two items per range (the first and the last it holds a part of), and the prefix sums.
-size_t attention_ws(int batch, int head_dim, bool e4m3, int sms) {
+// Partials of two items per range (the first and the last it holds a part of).
+size_t attention_ws(int head_dim, bool e4m3, int sms) {
     const size_t slots = (size_t)sms * attention_warps(head_dim, e4m3) * 2;
-    return slots * 16 * (size_t)head_dim * 4 + slots * 16 * 8 + ((size_t)batch + 1 + 3) / 4 * 16;
+    return slots * 16 * (size_t)head_dim * 4 + slots * 16 * 8;
 }
 
 bool attention_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
@@ -995,7 +1010,7 @@ wsm_status wsm_paged_attention_workspace(int batch, int head_dim, int cache_dtyp
     if (batch == 0 || !attention_may_cut(max_tokens, window)) return WSM_OK;
     int dev, sms;
     wsm_status st = device_sms(&dev, &sms);
-    if (st == WSM_OK) *bytes = attention_ws(batch, head_dim, cache_dtype == WSM_DTYPE_E4M3, sms);
+    if (st == WSM_OK) *bytes = attention_ws(head_dim, cache_dtype == WSM_DTYPE_E4M3, sms);
     return st;
 }
 
@@ -1039,7 +1054,7 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     if (a->batch > 1 && a->table_stride < 0) return op_fail(WSM_ERR_INVALID, "the table stride must not be negative");
     int dev, sms;
     if ((st = device_sms(&dev, &sms)) != WSM_OK) return st;
-    const size_t need = join ? attention_ws(a->batch, cache->head_dim, e8, sms) : 0;
+    const size_t need = join ? attention_ws(cache->head_dim, e8, sms) : 0;
     if (a->workspace_bytes < need)
         return op_fail(WSM_ERR_NOMEM, "workspace of %zu bytes is smaller than the %zu needed", a->workspace_bytes, need);
 
@@ -1057,7 +1072,6 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
         const size_t slots = (size_t)p.workers * 2;
         p.part_o = static_cast<float *>(a->workspace);
         p.part_ml = reinterpret_cast<float2 *>(p.part_o + slots * 16 * (size_t)D);
-        p.prefix = reinterpret_cast<int *>(p.part_ml + slots * 16);
     }
     p.q_row = step_of(a->q_strides[0], n_q[0]);
     p.q_head = step_of(a->q_strides[1], n_q[1]);
@@ -1097,7 +1111,10 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     const int rows = std::min(16, p.group);
     // a block for each row while there are few (and may be many partials), else one for all of an item's
     p.rows_per_cta = items * rows <= 2ll * sms ? 1 : rows;
-    p.join_split = kJoinWarps / p.rows_per_cta;
+    // a warp to a row for every two partials that an item has on average, four to a block at least (on a B200: 512
+    // sequences of 4 x 4 heads 68.7 us, 74.6 with sixteen warps to every block; 32 of 32 heads of 64 66.5 and 71.4)
+    const int cuts = (int)std::min<long long>(p.workers / items + 2, 1 << 20);
+    p.join_split = std::min(std::max((cuts + 1) / 2, (4 + p.rows_per_cta - 1) / p.rows_per_cta), kJoinWarps / p.rows_per_cta);
     const dim3 jg((unsigned)items, (unsigned)((rows + p.rows_per_cta - 1) / p.rows_per_cta));
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const bool bf = a->dtype == WSM_DTYPE_BF16;
