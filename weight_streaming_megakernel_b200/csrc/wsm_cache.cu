@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // do not depend on timing.
 //
 // Measured on a B200 (floor: the cache's bytes at the 6440 GB/s of a copy): one token over 131041 of a 16-bit cache of
-// 8 heads of 128 102 to 106 us (floor 83); 64 ragged sequences of up to 4000 tokens 36 to 42 us (22); 96 over an 8-bit cache
-// 56 to 60 us (34): the warps issue in 54 % of the cycles and the cache comes at 4.2 TB/s; one sequence of 37 tokens
+// 8 heads of 128 101 to 106 us (floor 83); 64 ragged sequences of up to 4000 tokens 36 to 42 us (22); 96 over an 8-bit cache
+// 53 to 60 us (34): the warps issue in 54 % of the cycles and the cache comes at 4.2 TB/s; one sequence of 37 tokens
 // 7.0 us.  About 4.5 us of each is the chain of reads that finds a warp its first tokens (lengths, then the table, then
 // keys), 5 to 6 the join's, which finds its items' places while the main kernel runs.  With the arithmetic taken out
 // the three large ones took 98, 39 and 54 us: what is left lies in the load path and these fixed costs.  A join by the
