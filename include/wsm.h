@@ -572,7 +572,10 @@ wsm_status wsm_chain_validate(const wsm_task *tasks, int n_tasks);
  *  - None of them allocates, synchronises, or keeps state between calls: where
  *    one needs scratch the caller passes it (any contents; nothing of it has
  *    to survive the call), so calls on different streams and graphs captured
- *    on one stream never share any.
+ *    on one stream never share any.  Scratch is free for any later call on the
+ *    stream, one with WSM_FLAG_INDEPENDENT included: such a call starts only
+ *    when the operator before it has used its scratch for the last time.
+ *    (Their other buffers are under that flag's promise like any call's.)
  *  - Strides are in elements and not negative; the last dimension of every
  *    tensor is contiguous.
  *  - Index tensors (slots, block_table, lengths, offsets, tokens) live on the

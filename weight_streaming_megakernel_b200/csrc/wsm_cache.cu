@@ -770,7 +770,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
     const int at = (before + kItemCost * b) * hq + item * (n + kItemCost);
     const int per = share_of((all + kItemCost * p.batch) * hq, p.workers);
     pdl_wait();                                         // (before any return: who comes next waits for this kernel alone)
-    pdl_launch_dependents();
+    // No trigger for the next launch: it comes when this kernel's blocks are through with the scratch, as that call may be
+    // one that waits for nothing (WSM_FLAG_INDEPENDENT) and may write there, the scratch being the caller's again.
     if (n <= kSnapGroups) return;                       // never cut
     // group g lies kItemCost + g past the item's place in the line; the ranges of the first and the last one
     const int w0 = (at + kItemCost) / per, w1 = (at + kItemCost + n - 1) / per;

@@ -365,7 +365,6 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
     }
     if (warp == 1) tmem_alloc(&tmem_base_sh, kExTmemCols);
     pdl_wait();                                         // the plan is there, and whatever came before it
-    pdl_launch_dependents();
     for (int e = threadIdx.x; e < p.experts; e += kExThreads) unit0[e] = p.rec[e].unit0;
     tc_fence_before();
     __syncthreads();
@@ -584,6 +583,10 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
     }
     tc_fence_before();
     __syncthreads();
+    // Only now, when this CTA is through with the scratch (its partials were performed before their unit's arrival was
+    // counted): the next call may be one that waits for nothing (WSM_FLAG_INDEPENDENT), and its outputs may lie in
+    // the scratch, which is the caller's again once this call has returned.
+    pdl_launch_dependents();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, kExTmemCols);
 }

@@ -54,7 +54,9 @@ static inline wsm_status op_fail(wsm_status code, const char *fmt, ...) {
 
 // One launch with programmatic dependent launch: every operator kernel waits for the kernel before it
 // (griddepcontrol.wait) before it touches global memory and lets the next one launch only after that, as
-// the GEMMs do, so stream order holds through any mix of them.
+// the GEMMs do, so stream order holds through any mix of them.  A kernel that is an operator's last to use the
+// caller's scratch lets the next one launch only when it is through with it: independent calls do not wait, and
+// the caller may have given the scratch to one.
 template <typename P>
 static inline wsm_status op_launch(void (*fn)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P &p,
                                    int cluster = 0) {
