@@ -714,10 +714,14 @@ typedef struct {
 } wsm_logprobs;
 wsm_status wsm_token_logprobs(const wsm_logprobs *args, wsm_stream_t stream);
 
-/* Synchronise `stream`, then report what the operators above recorded on the
- * current device, on any stream, since the last check, and clear it:
- * WSM_ERR_INVALID for an index out of range, WSM_ERR_TIMEOUT for a device-side
- * wait that ran out (*code the same; message in wsm_last_error()), else WSM_OK. */
+/* Synchronise `stream`, then report one error that the operators above recorded
+ * on the current device, on any stream, and clear that one: WSM_ERR_TIMEOUT for
+ * a device-side wait that ran out, before WSM_ERR_INVALID for an index out of
+ * range (*code the same; message in wsm_last_error()), else WSM_OK.  The first
+ * time-out and the first index out of range of each kind (cache and attention,
+ * experts, log probabilities) are kept until reported: ask until WSM_OK for all
+ * of them.  What a call on another stream records meanwhile is in this answer
+ * or a later one. */
 wsm_status wsm_operator_status(wsm_stream_t stream, int *code);
 
 /* ---------------------------------------------------------------- misc */

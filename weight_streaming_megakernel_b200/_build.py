@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["wsm_api.cu", "wsm_umma.cu", "wsm_stream.cu", "wsm_noalloc.cu", "wsm_die.cu",
-           "wsm_cache.cu", "wsm_experts.cu", "wsm_logprobs.cu"]
+           "wsm_cache.cu", "wsm_experts.cu", "wsm_logprobs.cu", "wsm_opstatus.cu"]
 HEADERS = ["wsm_internal.cuh", "wsm_tcgen05.cuh", "wsm_ops.cuh"]
 LIB = os.path.join(PKG, "libwsm.so")
 

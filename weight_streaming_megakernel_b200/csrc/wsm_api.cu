@@ -1160,10 +1160,6 @@ wsm_status encode_tiled(CUtensorMap *map, CUtensorMapDataType type, int rank, co
     if (r != CUDA_SUCCESS) return fail(WSM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return WSM_OK;
 }
-
-wsm_status cache_status_ptr(void **p);     // wsm_cache.cu
-wsm_status experts_status_ptr(void **p);   // wsm_experts.cu
-wsm_status logprobs_status_ptr(void **p);  // wsm_logprobs.cu
 }  // namespace wsm
 
 using namespace wsm;
@@ -1321,32 +1317,6 @@ wsm_status wsm_workspace_status(const void *workspace, size_t workspace_bytes, w
     if (h[0] == 0) return WSM_OK;
     if (code) *code = h[0];
     return fail(WSM_ERR_TIMEOUT, "device-side wait ran out in a call on this workspace (cta %d, site %d)", h[2], h[3]);
-}
-
-wsm_status wsm_operator_status(wsm_stream_t stream_, int *code) {
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    if (code) *code = 0;
-    static wsm_status (*const blocks[])(void **) = {cache_status_ptr, experts_status_ptr, logprobs_status_ptr};
-    static const char *const names[] = {"the paged cache or its attention", "the expert products", "the log probabilities"};
-    int first[kStatusWords] = {};
-    int which = 0;
-    for (int i = 0; i < 3; ++i) {
-        void *ptr = nullptr;
-        wsm_status st = blocks[i](&ptr);
-        if (st != WSM_OK) return st;
-        int h[kStatusWords] = {};
-        if ((st = read_clear_status(ptr, stream, h)) != WSM_OK) return st;
-        if (h[0] != 0 && first[0] == 0) {
-            memcpy(first, h, sizeof h);
-            which = i;
-        }
-    }
-    if (first[0] == 0) return WSM_OK;
-    if (code) *code = first[0];
-    if (first[0] == WSM_ERR_TIMEOUT)
-        return fail(WSM_ERR_TIMEOUT, "device-side wait ran out in %s (cta %d, site %d)", names[which], first[2], first[3]);
-    return fail(WSM_ERR_INVALID, "an index out of range in %s (row, sequence or expert %d, site %d)", names[which], first[1],
-                first[3]);
 }
 
 wsm_status wsm_debug_stall(int calls, unsigned long long limit_ns) {

@@ -11,7 +11,7 @@ namespace wsm {
 
 namespace {
 
-static __device__ int g_cache_status[kOpStatusInts];
+static __device__ unsigned long long g_cache_error;
 
 // ------------------------------------------------------------------ append
 
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             for (int i = 0; i < kAppendUnroll; ++i) {
                 if (slot[i] < 0) continue;              // no place: a padded row
                 if (slot[i] >= p.n_slots) {
-                    if (c == 0) record_op_error(g_cache_status, kCodeInvalid, (int)(t0 + i * step), kSiteSlot);
+                    if (c == 0) record_op_error(&g_cache_error, (int)(t0 + i * step), kSiteSlot);
                     continue;
                 }
                 long long page;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
     for (int b0 = 0; b0 < p.batch; b0 += NW * 32) {
         const int b = b0 + (int)threadIdx.x;
         int len = b < p.batch ? p.lengths[b] : 0;
-        if (blockIdx.x == 0 && len > p.max_tokens) record_op_error(g_cache_status, kCodeInvalid, b, kSiteLength);
+        if (blockIdx.x == 0 && len > p.max_tokens) record_op_error(&g_cache_error, b, kSiteLength);
         int v = span_of(p, len).groups;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         if ((k & 1) == 0) {
             const Pages now = ahead;
             const bool ok = now.in && (unsigned)now.page < (unsigned)p.num_pages;
-            if (now.in && !ok) record_op_error(g_cache_status, kCodeInvalid, now.seq, kSitePage);
+            if (now.in && !ok) record_op_error(&g_cache_error, now.seq, kSitePage);
             there = __ballot_sync(0xffffffffu, ok);
             const unsigned long long ko = ok ? (now.page * p.k_page + now.off * p.k_tok + now.head * p.k_head) * ESZ / 16 : 0;
             k_lo = (uint32_t)ko;
@@ -932,8 +932,8 @@ bool attention_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256
 
 }  // namespace
 
-wsm_status cache_status_ptr(void **p) {
-    WSM_OP_CUDA(cudaGetSymbolAddress(p, g_cache_status));
+wsm_status cache_error_ptr(void **p) {
+    WSM_OP_CUDA(cudaGetSymbolAddress(p, g_cache_error));
     return WSM_OK;
 }
 

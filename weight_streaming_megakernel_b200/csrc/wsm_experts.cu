@@ -35,7 +35,8 @@ namespace wsm {
 
 namespace {
 
-static __device__ int g_experts_status[kOpStatusInts];
+static __device__ int g_experts_status[kOpStatusInts];     // waits that ran out
+static __device__ unsigned long long g_experts_error;
 
 constexpr int kMaxExperts = 1024;
 constexpr int kTileN = 128;         // weight rows per tile (MMA M)
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kMaxExperts) experts_plan_kernel(const __grid_
         lo = lo0;
         for (int w = 0; w < (e >> 5); ++w) lo = max(lo, warp_tot[w]);
     }
-    if (have && (raw != hi || (e == 0 && raw0 != lo0))) record_op_error(g_experts_status, kCodeInvalid, e, kSiteOffsets);
+    if (have && (raw != hi || (e == 0 && raw0 != lo0))) record_op_error(&g_experts_error, e, kSiteOffsets);
     const int m = have ? hi - lo : 0;
     // The highest tiles read the least (for 256 rows of X 48 KB to a K box, for 64 24 KB), but a call with few of them
     // leaves SMs without: below one to three SMs, lower ones.  (On a B200, 400 rows of 4 experts of 1152 x 3944: 38 us
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kExThreads, 1) experts_kernel(const __grid_con
                 while (ld_acquire_gpu(reinterpret_cast<const unsigned int *>(&status[kStatusStallFlag])) == 0u &&
                        globaltimer() - t0 <= p.stall_ns)
                     __nanosleep(256);
-                record_op_error(status, kCodeTimeout, -1, kSiteStall);
+                record_error(status, kCodeTimeout, -1, kSiteStall);
                 abort_flag = 1;
                 aborted = true;
             }
@@ -615,6 +616,11 @@ ExLayout experts_layout(int rows, int experts, int sms) {
 
 wsm_status experts_status_ptr(void **p) {
     WSM_OP_CUDA(cudaGetSymbolAddress(p, g_experts_status));
+    return WSM_OK;
+}
+
+wsm_status experts_error_ptr(void **p) {
+    WSM_OP_CUDA(cudaGetSymbolAddress(p, g_experts_error));
     return WSM_OK;
 }
 

@@ -28,7 +28,7 @@ namespace wsm {
 
 namespace {
 
-static __device__ int g_logprobs_status[kOpStatusInts];
+static __device__ unsigned long long g_logprobs_error;
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpLoads == kFewRowsLoads ? 2 : 3)
             float lp = 0.f;
             if (token >= p.vocab) {
                 lp = NAN;
-                record_op_error(g_logprobs_status, kCodeInvalid, (int)row, kSiteToken);
+                record_op_error(&g_logprobs_error, (int)row, kSiteToken);
             } else if (token >= 0) {
                 lp = logprob_of(token_x);
             }
@@ -531,8 +531,8 @@ template <typename T> wsm_status run_logprobs(const LogprobsParams &p, int sms, 
 
 }  // namespace
 
-wsm_status logprobs_status_ptr(void **p) {
-    WSM_OP_CUDA(cudaGetSymbolAddress(p, g_logprobs_status));
+wsm_status logprobs_error_ptr(void **p) {
+    WSM_OP_CUDA(cudaGetSymbolAddress(p, g_logprobs_error));
     return WSM_OK;
 }
 

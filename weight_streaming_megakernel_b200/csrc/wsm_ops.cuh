@@ -20,20 +20,21 @@ wsm_status device_sms(int *dev, int *sms);      // wsm_api.cu: the current devic
 wsm_status encode_tiled(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
                         const cuuint64_t *strides, const cuuint32_t *box);  // wsm_api.cu: 128-byte swizzle
 
-// Device addresses of the operators' status blocks on the current device (each in its own source file).
-wsm_status cache_status_ptr(void **p);
-wsm_status experts_status_ptr(void **p);
-wsm_status logprobs_status_ptr(void **p);
+// Device addresses, on the current device, of what wsm_operator_status (wsm_opstatus.cu) takes: an error word of
+// each operator family for values out of range (record_op_error), and the block of the expert products' waits.
+wsm_status cache_error_ptr(void **p);     // wsm_cache.cu
+wsm_status experts_error_ptr(void **p);   // wsm_experts.cu
+wsm_status experts_status_ptr(void **p);  // wsm_experts.cu
+wsm_status logprobs_error_ptr(void **p);  // wsm_logprobs.cu
 
-// Status block of one operator family on one device, in the library's device image: [0] the first error
-// code since the host last read it (sticky), [1] a number that says which (the sequence, row or expert),
-// [2] the CTA, [3] the site; [5] never written (what a stalled launch waits on).  The same words as the
-// GEMMs' status block (wsm_internal.cuh); [4] is not used: no operator's launch consults another's errors.
+// The block of an operator's waits on one device, in the library's device image: [0] the code of the first one that
+// ran out since the host last read it (sticky), [2] the CTA, [3] the site; [5] never written (what a stalled launch
+// waits on).  The same words as the GEMMs' status block (wsm_internal.cuh); [4] is not used: no operator's launch
+// consults another's errors.
 constexpr int kOpStatusInts = 16;
 
-// Sites of the operators' errors (status[3]).
+// Sites of the operators' errors.
 enum : int { kSitePage = 32, kSiteLength = 33, kSiteSlot = 34, kSiteOffsets = 35, kSiteToken = 36 };
-constexpr int kCodeInvalid = 1;  // == WSM_ERR_INVALID
 
 static inline wsm_status op_fail(wsm_status code, const char *fmt, ...) {
     char buf[512];
@@ -98,13 +99,10 @@ static inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cas
 
 #if defined(__CUDACC__)
 
-// Record a device-side error: the first since the host last read the block.
-__device__ __forceinline__ void record_op_error(int *status, int code, int which, int site) {
-    if (atomicCAS(status, 0, code) == 0) {
-        status[1] = which;
-        status[2] = (int)blockIdx.x;
-        status[3] = site;
-    }
+// Record a value out of range: the first of the family since the host last took one.  The site and which (the
+// sequence, row or expert) in one word: who takes it gets both or neither.
+__device__ __forceinline__ void record_op_error(unsigned long long *word, int which, int site) {
+    atomicCAS(word, 0ull, (unsigned long long)site << 32 | (uint32_t)which);
 }
 
 // 2^y: the hardware approximation, relative error 2^-22, subnormal results 0

@@ -325,10 +325,11 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
 
 
 def operator_status(stream=None) -> int:
-    """Synchronise the stream; 0, or the first error that a decode-step
-    operator recorded on the current device, on any stream, since the last
-    check: WSM_ERR_INVALID for an index out of range (last_error() says
-    which), WSM_ERR_TIMEOUT for a device-side wait that ran out."""
+    """Synchronise the stream; 0, or an error that a decode-step operator
+    recorded on the current device, on any stream: WSM_ERR_TIMEOUT for a
+    device-side wait that ran out, before WSM_ERR_INVALID for an index out of
+    range (last_error() says where).  That error is cleared; one of another
+    kind stays for the next query, so ask until 0 for all of them."""
     code = ctypes.c_int(0)
     rc = _wsm.lib().wsm_operator_status(_wsm._stream_handle(stream), ctypes.byref(code))
     if rc not in (_wsm.WSM_OK, _wsm.WSM_ERR_INVALID, _wsm.WSM_ERR_TIMEOUT):
