@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["wsm_api.cu", "wsm_umma.cu", "wsm_stream.cu", "wsm_noalloc.cu", "wsm_die.cu",
            "wsm_cache.cu", "wsm_experts.cu", "wsm_logprobs.cu", "wsm_opstatus.cu"]
-HEADERS = ["wsm_internal.cuh", "wsm_tcgen05.cuh", "wsm_ops.cuh"]
+HEADERS = ["wsm_internal.cuh", "wsm_tcgen05.cuh", "wsm_ops.cuh", "wsm_deal.cuh"]
 LIB = os.path.join(PKG, "libwsm.so")
 
 NVCC_FLAGS = [

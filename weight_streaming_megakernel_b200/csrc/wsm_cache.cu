@@ -1,6 +1,7 @@
 // wsm_cache.cu -- the paged key-value cache: writing new tokens into it (wsm_paged_cache_append) and the
 // attention of one new token of each sequence over it (wsm_paged_attention), the step between the qkv and
 // the o projection of a decode step.
+#include "wsm_deal.cuh"
 #include "wsm_ops.cuh"
 
 #include <algorithm>
@@ -134,13 +135,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // last block to arrive instead of a second launch: the same on ragged and long batches, 71 us on the 8-bit one, whose
 // registers it took.
 
-constexpr int kGroup = 16;          // tokens a warp takes at a time (the MMA's k)
 constexpr int kMaxBatch = 4096;     // sequences per call: their group prefix sums sit in shared memory
-constexpr int kMinShare = 4;        // least length of a warp's range: no more than the shortest item's
-constexpr int kSnapGroups = 8;      // items of up to this many groups (128 tokens) are never cut
-// What beginning and ending an item costs a warp, in groups: counted when the work is dealt out, so that a warp
-// with many short sequences does not finish last.
-constexpr int kItemCost = 3;
 // Weights are 2^(score - reference), the reference kBelow under the running maximum: so a weight of 2^-31 of the
 // largest is still an fp16 number, and the largest is a power of two, which no rounding touches -- where one token
 // has nearly all the weight, the output is its value.  (A reference that moves only when the maximum has left it by
@@ -169,65 +164,6 @@ struct AttnParams {
     int workers;
     int rows_per_cta, join_split;   // join: rows of an item one block takes, and the warps for each
 };
-
-// The tokens a sequence attends to, [first, len), and its groups: kGroup-aligned from first down.
-struct Span {
-    int first, len, base, groups;
-};
-__device__ __forceinline__ Span span_of(const AttnParams &p, int len) {
-    Span s;
-    s.len = min(max(len, 0), p.max_tokens);
-    s.first = p.window > 0 ? max(0, s.len - p.window) : 0;
-    s.base = s.first & ~(kGroup - 1);
-    s.groups = (s.len - s.base + kGroup - 1) / kGroup;  // 0 for an empty sequence
-    return s;
-}
-
-// The work in a line: sequence b's items follow one another, each kItemCost + groups long, so b begins at
-// (prefix[b] + kItemCost * b) * hq with prefix the groups before b.  (At most 2^31 - 1 in all: checked by the host.)
-__device__ __forceinline__ int line_of(const int *prefix, int hq, int b) { return (prefix[b] + kItemCost * b) * hq; }
-
-// Length of a warp's range.
-__device__ __forceinline__ int share_of(int total, int workers) {
-    const int per = (total + workers - 1) / workers;
-    return per < kMinShare ? kMinShare : per;
-}
-
-// The sequence at place `pos` of the line.
-__device__ __forceinline__ int seq_of(const int *prefix, int batch, int hq, int pos) {
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (line_of(prefix, hq, mid + 1) > pos) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
-// Where range w begins: sequence, item and group.  A range that would begin within an item's fixed cost, or
-// within a short item, begins with the item.
-struct Place {
-    int b, item, g;
-};
-__device__ __forceinline__ Place place_of(const int *prefix, int batch, int hq, int total, int per, int w) {
-    Place r;
-    const long long pos = (long long)w * per;
-    if (pos >= total) {
-        r.b = batch;
-        r.item = r.g = 0;
-        return r;
-    }
-    r.b = seq_of(prefix, batch, hq, (int)pos);
-    const int n = prefix[r.b + 1] - prefix[r.b], off = (int)pos - line_of(prefix, hq, r.b);
-    r.item = off / (n + kItemCost);
-    r.g = n <= kSnapGroups ? 0 : max(0, off - r.item * (n + kItemCost) - kItemCost);
-    return r;
-}
-// Groups before a place.
-__device__ __forceinline__ int groups_before(const int *prefix, int hq, const Place &r, int batch) {
-    if (r.b >= batch) return prefix[batch] * hq;
-    return prefix[r.b] * hq + r.item * (prefix[r.b + 1] - prefix[r.b]) + r.g;
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -313,7 +249,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         const int b = b0 + (int)threadIdx.x;
         int len = b < p.batch ? p.lengths[b] : 0;
         if (blockIdx.x == 0 && len > p.max_tokens) record_op_error(&g_cache_error, b, kSiteLength);
-        int v = span_of(p, len).groups;
+        int v = span_of(p.max_tokens, p.window, len).groups;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -366,7 +302,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         litem = lg = 0;
     }
     const Place start = {lb, litem, lg};
-    Span ls = span_of(p, p.lengths[lb]);
+    Span ls = span_of(p.max_tokens, p.window, p.lengths[lb]);
     const int start_groups = ls.groups;
     int next_len = lb + 1 < p.batch ? p.lengths[lb + 1] : 0;    // fetched a sequence ahead
     // Two groups at a time, looked up two groups ahead: lanes 0-15 hold the page of the even group's tokens, lanes
@@ -404,7 +340,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
                         ++lb;
                         int len = next_len;
                         while (prefix[lb + 1] == prefix[lb]) len = p.lengths[++lb];
-                        ls = span_of(p, len);
+                        ls = span_of(p.max_tokens, p.window, len);
                         next_len = lb + 1 < p.batch ? p.lengths[lb + 1] : 0;
                     }
                 }
@@ -572,10 +508,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             }
             return;
         }
-        // first slot: the range begins in this item; else the item begins in the range (a range holds parts of one
-        // item of either kind at most)
-        const int slot = worker * 2 +
-                         ((long long)worker * per >= line_of(prefix, hq, cb) + citem * (cgroups + kItemCost) ? 0 : 1);
+        const int slot = slot_of(worker, per, line_of(prefix, hq, cb) + citem * (cgroups + kItemCost));
         float *po = p.part_o + (size_t)slot * 16 * D;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -753,7 +686,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
     // for what came before, so the lengths are there.
     int before = 0, all = 0;
     for (int i = threadIdx.x; i < p.batch; i += (int)blockDim.x) {
-        const int g = span_of(p, p.lengths[i]).groups;
+        const int g = span_of(p.max_tokens, p.window, p.lengths[i]).groups;
         all += g;
         before += i < b ? g : 0;
     }
@@ -766,17 +699,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
         before += groups[w].x;
         all += groups[w].y;
     }
-    const int n = span_of(p, p.lengths[b]).groups;
+    const int n = span_of(p.max_tokens, p.window, p.lengths[b]).groups;
     const int at = (before + kItemCost * b) * hq + item * (n + kItemCost);
     const int per = share_of((all + kItemCost * p.batch) * hq, p.workers);
     pdl_wait();                                         // (before any return: who comes next waits for this kernel alone)
     // No trigger for the next launch: it comes when this kernel's blocks are through with the scratch, as that call may be
     // one that waits for nothing (WSM_FLAG_INDEPENDENT) and may write there, the scratch being the caller's again.
     if (n <= kSnapGroups) return;                       // never cut
-    // group g lies kItemCost + g past the item's place in the line; the ranges of the first and the last one
-    const int w0 = (at + kItemCost) / per, w1 = (at + kItemCost + n - 1) / per;
+    const Ranges ranges = ranges_of(at, n, per);
+    const int w0 = ranges.first, w1 = ranges.last;
     if (w0 == w1) return;                               // one range holds it
-    const int slot0 = w0 * 2 + ((long long)w0 * per >= at ? 0 : 1);
+    const int slot0 = slot_of(w0, per, at);
     const int split = p.join_split, wr = warp / split, ws = warp - wr * split;
     const int r = (int)blockIdx.y * p.rows_per_cta + wr;
     const bool mine = wr < p.rows_per_cta && r < rows;
