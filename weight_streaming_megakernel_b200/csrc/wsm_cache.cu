@@ -137,10 +137,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
 constexpr int kMaxBatch = 4096;     // sequences per call: their group prefix sums sit in shared memory
 // Weights are 2^(score - reference), the reference kBelow under the running maximum: so a weight of 2^-31 of the
-// largest is still an fp16 number, and the largest is a power of two, which no rounding touches -- where one token
-// has nearly all the weight, the output is its value.  (A reference that moves only when the maximum has left it by
-// far saves most rescalings, 2 % of a call over an 8-bit cache, but rounds the largest weight: errors 1.3 times.)
+// largest is still an fp16 number, and the largest is 2^kBelow but for the rounding of its score, too little for the
+// 16 bits to show -- where one token has nearly all the weight, the output is its value.  (A reference that moves only
+// when the maximum has left it by far saves most rescalings, 2 % of a call over an 8-bit cache, but rounds the largest
+// weight: errors 1.3 times.)
 constexpr float kBelow = 7.f;
+// The reference comes from a rounded score, the weight's exponent from the unrounded one (one multiply-add).  They
+// differ by half a step of the score: 2^-15 up to kFar, but tens from 2^29 on, where a weight would overflow or vanish.
+// Past kFar the score is rounded before the reference is taken from it, so the largest weight is a whole power of two
+// (2^7, and 2^0 to 2^8 from 2^24 on, where the reference itself is rounded).
+constexpr float kFar = 1024.f;
 
 struct AttnParams {
     const uint8_t *Q;
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
     attention_kernel(const __grid_constant__ AttnParams p) {
     using Geo = AttnGeo<D, kE4m3 ? 1 : 2>;
     // With an 8-bit cache both products run in fp16 whatever the queries' type: every e4m3 value is one, and
-    // 16-bit weights in [0, 1] lose less there than in bf16.  A bf16 query row is brought into fp16's range by
+    // 16-bit weights of 2^kBelow or so lose less there than in bf16.  A bf16 query row is brought into fp16's range by
     // a power of two, which the score factor takes back: exact but for elements 2^-30 of the row's largest.
     using M = typename std::conditional<kE4m3, __half, T>::type;
     constexpr int ESZ = kE4m3 ? 1 : 2;
@@ -397,6 +403,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
     uint32_t qa[KS][4];
     float o[2 * KS][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, f0 = 0.f, f1 = 0.f;
+    bool far = false;                                   // a reference of the warp's is past kFar
     auto begin_item = [&]() {
         const int h = p.q_tiles == 1 ? citem : citem / p.q_tiles, qt = citem - h * p.q_tiles;
         const int rows = min(16, p.group - qt * 16);
@@ -452,6 +459,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
         for (int i = 0; i < 2 * KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         m0 = m1 = -INFINITY;
         l0 = l1 = 0.f;
+        far = false;
         // the following item's queries into L1 meanwhile (the next heads of this sequence, or the next sequence's)
         const T *qn = citem + 1 < hq ? q + (long long)rows * p.q_head
                                      : reinterpret_cast<const T *>(p.Q) + min(cb + 1, p.batch - 1) * p.q_row;
@@ -591,8 +599,8 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
                 x1[j] = in ? x1[j] : -INFINITY;
             }
         }
-        float n0 = fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3])) * f0;
-        float n1 = fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3])) * f1;
+        float n0 = __fmul_rn(fmaxf(fmaxf(x0[0], x0[1]), fmaxf(x0[2], x0[3])), f0);
+        float n1 = __fmul_rn(fmaxf(fmaxf(x1[0], x1[1]), fmaxf(x1[2], x1[3])), f1);
         // (a thread of a row's four sees its own four scores: the vote is over all, the maximum is shared only then)
         if (__any_sync(0xffffffffu, n0 > m0 + kBelow || n1 > m1 + kBelow)) {
 #pragma unroll
@@ -606,6 +614,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             const float a0 = n0 == m0 ? 1.f : ex2(m0 - n0), a1 = n1 == m1 ? 1.f : ex2(m1 - n1);
             m0 = n0;
             m1 = n1;
+            far = __any_sync(0xffffffffu, (fabsf(m0) > kFar && m0 != -INFINITY) || (fabsf(m1) > kFar && m1 != -INFINITY));
             l0 *= a0;
             l1 *= a1;
 #pragma unroll
@@ -617,10 +626,23 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             }
         }
         const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+        if (!far) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x0[j] = fmaf(x0[j], f0, -z0);
+                x1[j] = fmaf(x1[j], f1, -z1);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x0[j] = __fsub_rn(__fmul_rn(x0[j], f0), z0);
+                x1[j] = __fsub_rn(__fmul_rn(x1[j], f1), z1);
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            x0[j] = ex2(fmaf(x0[j], f0, -z0));
-            x1[j] = ex2(fmaf(x1[j], f1, -z1));
+            x0[j] = ex2(x0[j]);
+            x1[j] = ex2(x1[j]);
             l0 += x0[j];
             l1 += x1[j];
         }
