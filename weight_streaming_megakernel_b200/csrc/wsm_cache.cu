@@ -130,7 +130,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // 8 heads of 128 101 to 106 us (floor 83); 64 ragged sequences of up to 4000 tokens 36 to 42 us (22); 96 over an 8-bit cache
 // 53 to 60 us (34): the warps issue in 54 % of the cycles and the cache comes at 4.2 TB/s; one sequence of 37 tokens
 // 7.0 us.  About 4.5 us of each is the chain of reads that finds a warp its first tokens (lengths, then the table, then
-// keys), 5 to 6 the join's, which finds its items' places while the main kernel runs.  With the arithmetic taken out
+// keys), 5 to 6 the join's, which reads its items' places as the main kernel left them.  (Every block of the join
+// summing the lengths itself is as fast up to 256 sequences, but grows with the square: 4096 sequences of 20 tokens of
+// 32 over 8 heads of 128 took 264 us, 145 now; of 130 tokens 505 and 382.)  With the arithmetic taken out
 // the three large ones took 98, 39 and 54 us: what is left lies in the load path and these fixed costs.  A join by the
 // last block to arrive instead of a second launch: the same on ragged and long batches, 71 us on the 8-bit one, whose
 // registers it took.
@@ -156,6 +158,8 @@ struct AttnParams {
     const int *table, *lengths;
     float *part_o;                  // [workers][2][16][D]
     float2 *part_ml;                // [workers][2][16]: reference (base 2) and sum
+    int *prefix;                    // [batch + 2], for the join (NULL: none follows): the groups before each sequence and
+                                    // in all, and the length of a range
     long long q_row, q_head, o_row, o_head;        // elements
     long long k_page, k_tok, k_head, v_page, v_tok, v_head;
     long long table_stride;
@@ -269,8 +273,14 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
             if (w < warp) before += s;
             carry += s;
         }
-        if (b < p.batch) prefix[b + 1] = before + v;
-        if (b == 0) prefix[0] = 0;
+        if (b < p.batch) {
+            prefix[b + 1] = before + v;
+            if (blockIdx.x == 0 && p.prefix) p.prefix[b + 1] = before + v;
+        }
+        if (b == 0) {
+            prefix[0] = 0;
+            if (blockIdx.x == 0 && p.prefix) p.prefix[0] = 0;
+        }
         __syncthreads();
     }
 
@@ -278,6 +288,7 @@ __global__ void __launch_bounds__(AttnGeo<D, kE4m3 ? 1 : 2>::kWarps * 32, 1)
     const int worker = warp * (int)gridDim.x + (int)blockIdx.x;
     const int total = line_of(prefix, hq, p.batch);
     const int per = share_of(total, p.workers);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.prefix) p.prefix[p.batch + 1] = per;
 
     // ---- sequences without a token to attend to: zeros, and the empty sum's logarithm
     for (int b = worker; b < p.batch; b += p.workers) {
@@ -698,43 +709,30 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ AttnParams p) {
     __shared__ float4 sum[kJoinWarps][D / 4];
     __shared__ float2 ml[kJoinWarps];
-    __shared__ int2 groups[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hq = p.kv_heads * p.q_tiles;
     const int b = (int)blockIdx.x / hq, item = (int)blockIdx.x - b * hq;
     const int h = p.q_tiles == 1 ? item : item / p.q_tiles, qt = item - h * p.q_tiles;
     const int rows = min(16, p.group - qt * 16);
-    // Where the item lies in the line, while the main kernel runs: its blocks let this one begin after their own wait
-    // for what came before, so the lengths are there.
-    int before = 0, all = 0;
-    for (int i = threadIdx.x; i < p.batch; i += (int)blockDim.x) {
-        const int g = span_of(p.max_tokens, p.window, p.lengths[i]).groups;
-        all += g;
-        before += i < b ? g : 0;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    all = __reduce_add_sync(0xffffffffu, all);
-    if (lane == 0) groups[warp] = make_int2(before, all);
-    __syncthreads();
-    before = all = 0;
-    for (int w = 0; w < (int)blockDim.x >> 5; ++w) {
-        before += groups[w].x;
-        all += groups[w].y;
-    }
-    const int n = span_of(p.max_tokens, p.window, p.lengths[b]).groups;
-    const int at = (before + kItemCost * b) * hq + item * (n + kItemCost);
-    const int per = share_of((all + kItemCost * p.batch) * hq, p.workers);
+    // what needs no data, and the parameters, before the wait
+    const int split = p.join_split, wr = warp / split, ws = warp - wr * split;
+    const int r = (int)blockIdx.y * p.rows_per_cta + wr;
+    const bool mine = wr < p.rows_per_cta && r < rows;
+    const int *prefix = p.prefix, *of_b = prefix + b, *of_all = prefix + p.batch + 1;
+    const float *part_o = p.part_o;
+    const float2 *part_ml = p.part_ml;
+    asm volatile("" : "+l"(of_b), "+l"(of_all), "+l"(part_o), "+l"(part_ml));
     pdl_wait();                                         // (before any return: who comes next waits for this kernel alone)
     // No trigger for the next launch: it comes when this kernel's blocks are through with the scratch, as that call may be
     // one that waits for nothing (WSM_FLAG_INDEPENDENT) and may write there, the scratch being the caller's again.
+    // (through L1: all warps of all blocks read the same few words)
+    const int before = of_b[0], n = of_b[1] - before, per = of_all[0];
     if (n <= kSnapGroups) return;                       // never cut
+    const int at = (before + kItemCost * b) * hq + item * (n + kItemCost);      // where the item lies in the line
     const Ranges ranges = ranges_of(at, n, per);
     const int w0 = ranges.first, w1 = ranges.last;
     if (w0 == w1) return;                               // one range holds it
     const int slot0 = slot_of(w0, per, at);
-    const int split = p.join_split, wr = warp / split, ws = warp - wr * split;
-    const int r = (int)blockIdx.y * p.rows_per_cta + wr;
-    const bool mine = wr < p.rows_per_cta && r < rows;
     constexpr int NV = (D / 4 + 31) / 32;               // float4 columns per lane
     float m = -INFINITY, l = 0.f;
     float4 acc[NV] = {};
@@ -746,11 +744,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
             for (int u = 0; u < kJoinUnroll; ++u) {
                 const int w = wb + u * split;
                 const size_t slot = (size_t)(w == w0 ? slot0 : 2 * w) * 16 + r;
-                x[u] = w <= w1 ? __ldcg(&p.part_ml[slot]) : make_float2(-INFINITY, 0.f);
+                x[u] = w <= w1 ? __ldcg(&part_ml[slot]) : make_float2(-INFINITY, 0.f);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     v[u][i] = (w <= w1 && i * 32 + lane < D / 4)
-                                  ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot * D) + i * 32 + lane)
+                                  ? __ldcg(reinterpret_cast<const float4 *>(part_o + slot * D) + i * 32 + lane)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float mn = m;
@@ -877,10 +875,10 @@ bool attention_may_cut(long long max_tokens, int window) {
     return (span + kGroup - 1) / kGroup > kSnapGroups;
 }
 
-// Partials of two items per range (the first and the last it holds a part of).
+// Partials of two items per range (the first and the last it holds a part of), and the sequences' places in the line.
 size_t attention_ws(int head_dim, bool e4m3, int sms) {
     const size_t slots = (size_t)sms * attention_warps(head_dim, e4m3) * 2;
-    return slots * 16 * (size_t)head_dim * 4 + slots * 16 * 8;
+    return slots * 16 * (size_t)head_dim * 4 + slots * 16 * 8 + (kMaxBatch + 2) * sizeof(int);
 }
 
 bool attention_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
@@ -1028,6 +1026,7 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
         const size_t slots = (size_t)p.workers * 2;
         p.part_o = static_cast<float *>(a->workspace);
         p.part_ml = reinterpret_cast<float2 *>(p.part_o + slots * 16 * (size_t)D);
+        p.prefix = reinterpret_cast<int *>(p.part_ml + slots * 16);
     }
     p.q_row = step_of(a->q_strides[0], n_q[0]);
     p.q_head = step_of(a->q_strides[1], n_q[1]);
