@@ -64,14 +64,21 @@ constexpr float kFar = 65536.f;
 struct Stat {
     float m, r, l, u;
 };
-__device__ __forceinline__ float base_of(float m) { return fminf(fmaxf(m, -kFar), kFar) * kLog2e; }
+// (rounded by itself: contracted with a sum it would be another number in every place)
+__device__ __forceinline__ float base_of(float m) { return __fmul_rn(fminf(fmaxf(m, -kFar), kFar), kLog2e); }
 // y of an element by a maximum past kFar: differences of the elements themselves, as anything else vanishes
 __device__ __forceinline__ float far_y(float x, float m) { return (x - m) * kLog2e; }
+// What the rounding of r adds to every y by a maximum of m: up to 2^-8 next to kFar, nothing past it.
+__device__ __forceinline__ float y_offset(float m) { return fabsf(m) > kFar ? 0.f : fmaf(m, kLog2e, -base_of(m)); }
 // l and u move to a larger maximum; nothing summed so far (or a weight that vanishes) leaves nothing.
 __device__ __forceinline__ void rebase(Stat &s, float m) {
-    const bool far = fabsf(m) > kFar || fabsf(s.m) > kFar;
     const float r = base_of(m);
-    const float d = fmaxf(far ? far_y(s.m, m) : s.r - r, -200.f), f = ex2(d);
+    float d = s.r - r;
+    // (across the border: what one side's rounding added is taken off, what the other's adds put on; with nothing summed
+    // so far any d will do)
+    if (fabsf(m) > kFar || (fabsf(s.m) > kFar && s.m > -INFINITY)) d = far_y(s.m, m) + (y_offset(m) - y_offset(s.m));
+    d = fmaxf(d, -200.f);
+    const float f = ex2(d);
     s.u = (s.u + s.l * d) * f;
     s.l *= f;
     s.m = m;
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpLoads == kFewRowsLoads ? 2 : 3)
     s.u = __shfl_sync(0xffffffffu, s.u, 0);
     const bool none = s.l == 0.f;                       // no element above -infinity
     const float log_l = none ? 0.f : log2f(s.l);
-    const float from = (fabsf(s.m) > kFar ? 0.f : fmaf(s.m, kLog2e, -s.r)) - log_l;
+    const float from = y_offset(s.m) - log_l;
     auto logprob_of = [&](float x) {
         // x - m as it is; ln 2 times the rounding that r holds (see Stat) less the sum's logarithm
         return none ? -INFINITY : (x - s.m) + from * kLn2;
