@@ -1,4 +1,5 @@
-"""Token log probabilities: logits on both sides of the border between the kernel's two forms of an element's exponent."""
+"""Token log probabilities: more rows than the GPU takes at once, and logits on both sides of the border between the
+kernel's two forms of an element's exponent."""
 import math
 
 import pytest
@@ -26,6 +27,26 @@ def check(x, t, tops, what=""):
     for top in tops:
         got = wsm.token_logprobs(x, t, top=top)
         ref.check_logprobs(got, (lp, ent, ids[:, :top], best[:, :top]), x, f"{what} top {top}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab", [9, 1003, 9001])
+def test_a_second_wave_of_rows(dtype, vocab):
+    """Twice as many rows as the SMs hold blocks (three each), hard ones among them all along."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 2 * 3 * sms + 1
+    g = torch.Generator().manual_seed(vocab)
+    x = (torch.randn(rows, vocab, generator=g) * 3).to(dtype).to(DEV)
+    t = torch.randint(vocab, (rows,), generator=g).to(DEV)
+    x[::50] = 1.0                                       # all alike
+    x[1::50] = -math.inf                                # nothing left
+    x[2::50, vocab // 3:] = -math.inf
+    x[3::50] = torch.arange(vocab, device=DEV).to(dtype)    # rising
+    x[4::50, vocab // 2:] = torch.finfo(dtype).min
+    x[5::50, vocab // 2] = math.nan
+    t[6::50] = -1
+    check(x, t, sorted({0, min(3, vocab), min(32, vocab)}))
+    assert wsm.operator_status() == 0
 
 
 @pytest.mark.parametrize("vocab", [2, 5, 64, 1003, 40000, 200003])
