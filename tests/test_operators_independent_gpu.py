@@ -1,5 +1,6 @@
 """Independent GEMMs (WSM_FLAG_INDEPENDENT, which wait for nothing) behind the decode-step operators: they may be given the
-memory that an operator used as scratch, so they start only when it is through with it."""
+memory that an operator used as scratch, so they start only when it is through with it; and independent GEMMs whose output
+the library allocates, in memory that a call before may still read."""
 import time
 
 import pytest
@@ -99,3 +100,41 @@ def test_independent_call_that_writes_the_freed_scratch(op, captured):
         assert torch.equal(out, want)
         assert (y.float() - want_y.float()).abs().max() <= 2.0 ** -7 * want_y.float().abs().max()
     assert wsm.operator_status() == 0 and wsm.stream_status() == 0
+
+
+def test_independent_call_that_allocates_its_output_waits():
+    """The output's memory is the allocator's choice, so the caller could not promise that no call before reads it: the call
+    starts after them.  (The GEMM before it is held by the stall hook; the memory is that of a tensor dropped before.)"""
+    x, w = normal(16, 512, seed=2), normal(2048, 512, seed=3)
+    want = wsm.skinny_gemm(x, w, torch.empty(16, 2048, dtype=torch.bfloat16, device=DEV), flags=IND)
+    first = wsm.skinny_gemm(x, w)
+    seen = torch.empty(want.shape, dtype=want.dtype, pin_memory=True)
+    side = torch.cuda.Stream()
+    old = torch.full_like(want, 3.0)
+    at = old.data_ptr()
+    torch.cuda.synchronize()
+    wsm.debug_stall(1, 1_000_000_000)
+    wsm.skinny_gemm(x, w, first)
+    del old
+    y = wsm.skinny_gemm(x, w, flags=IND)
+    assert y.data_ptr() == at
+    time.sleep(0.2)
+    with torch.cuda.stream(side):
+        seen.copy_(y, non_blocking=True)
+    side.synchronize()
+    assert (seen == 3.0).all()
+    assert wsm.stream_status() == wsm.WSM_ERR_TIMEOUT
+    assert torch.equal(y, want)
+
+
+def test_independent_calls_behind_one_that_allocates():
+    """They run beside it, and later work still comes after all of them."""
+    x, w = normal(16, 512, seed=2), normal(2048, 512, seed=3)
+    want = wsm.skinny_gemm(x, w, flags=IND)
+    outs = []
+    for _ in range(20):
+        outs.append(wsm.skinny_gemm(x, w, flags=IND))
+        outs += [wsm.skinny_gemm(x, w, torch.empty_like(want), flags=IND) for _ in range(3)]
+    total = torch.stack(outs)
+    assert (total == want).all()
+    assert wsm.stream_status() == 0

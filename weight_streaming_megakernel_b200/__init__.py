@@ -246,7 +246,9 @@ def skinny_gemm(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor] = No
     """Y = X @ W.T on the current (or given) stream; returns Y.  With
     epilogue=EPI_SILU_MUL, W is the fused gate+up weight (rows interleaved in
     blocks of 8) and Y is [M, N/2] = silu(gate) * up; with EPI_RESIDUAL,
-    Y = X @ W.T + r."""
+    Y = X @ W.T + r.  With FLAG_INDEPENDENT give y: a y allocated here may be
+    memory that calls queued before still read, so the call then starts after
+    them (and runs beside those that follow)."""
     _check_operand("x", x)
     _check_operand("w", w)
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
@@ -256,6 +258,10 @@ def skinny_gemm(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor] = No
     ny = N // 2 if epilogue == EPI_SILU_MUL else N
     if y is None:
         y = torch.empty(M, ny, dtype=torch.bfloat16, device=x.device)
+        if flags & FLAG_INDEPENDENT:
+            # The allocator may hand out memory that a call queued before still reads (a tensor dropped since), and the
+            # caller's promise cannot cover a buffer that is picked here: the launch waits for them.
+            flags |= FLAG_NO_PDL
     _check_operand("y", y)
     if tuple(y.shape) != (M, ny):
         raise ValueError(f"y must be [{M}, {ny}]")
