@@ -652,7 +652,7 @@ typedef struct {
     int batch, heads, max_pages;
     int window;              /* 0: no window */
     int dtype;               /* of Q and O: WSM_DTYPE_BF16 or _FP16; a 16-bit cache has the same */
-    float scale;
+    float scale;             /* finite, and so scale * k_scale * log2(e) in fp32 */
 } wsm_attention;
 /* Scratch for sequences of up to max_tokens (max_pages * page_size) tokens on the current device: *bytes, 0
  * where no sequence can be long enough to be cut. */

@@ -91,3 +91,29 @@ def test_scores_that_grow_past_the_border(dtype, cache):
     q = q * torch.tensor([2.0 ** -14, 1.0, 2.0 ** -4, 1.0, 2.0 ** -7, 2.0 ** -14], dtype=dtype, device=DEV)[:, None]
     out = wsm.paged_attention(q, k, v, table, lengths, scale=2.0 ** 26)
     assert torch.equal(out, want.to(dtype))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("scale", [0.0, -0.0, 2.0 ** -149])
+def test_a_scale_of_nothing_is_a_mean(dtype, cache, scale):
+    """All scores vanish, whatever the queries and keys: every token has the same weight."""
+    size = 2.0 ** 60 if dtype == torch.bfloat16 else 2.0 ** 12
+    q, k, v, table, lengths, _ = make([300, 1, 20], (0.5,), 15, dtype, cache, seed=3)
+    if cache is None:
+        k = (k.double() * size).to(dtype)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = wsm.paged_attention((q.double() * size).to(dtype), k, v, table, lengths, scale=scale, lse=lse)
+    values = v.view(3, -1, 2, 64).double()
+    for b, n in enumerate(lengths.tolist()):
+        want = values[b, :n].mean(0).repeat_interleave(3, 0)
+        # equal weights, whole powers of two or off by the exponential's 2^-22, and n fp32 additions
+        off = 2.0 ** -9 if dtype == torch.bfloat16 else 2.0 ** -12
+        slack = (n + 8) * 2.0 ** -22 * values[b, :n].abs().mean(0).repeat_interleave(3, 0)
+        assert ((out[b].double() - want).abs() <= 2 * off * want.abs() + slack + 2.0 ** -25).all()
+        assert (lse[b].double() - math.log(n)).abs().max() <= 2.0 ** -20
+
+
+def test_a_factor_past_fp32_is_refused():
+    q, k, v, table, lengths, _ = make([20], (0.5,), 15, torch.float16, E4M3, seed=3)
+    with pytest.raises(wsm.WsmError, match="past fp32"):
+        wsm.paged_attention(q, k, v, table, lengths, scale=2.0 ** 127, k_scale=4.0)

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <type_traits>
 
 namespace wsm {
@@ -989,6 +990,9 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     if (max_tokens > 0x7fffffffll - kGroup || (max_tokens / kGroup + 1 + kItemCost) * std::max(a->batch, 1) * ((long long)cache->kv_heads * ((a->heads / cache->kv_heads + 15) / 16)) > 0x7fffffffll)
         return op_fail(WSM_ERR_UNSUPPORTED, "%d sequences of up to %lld tokens are too many", a->batch, max_tokens);
     if (!(a->scale > -INFINITY) || !(a->scale < INFINITY)) return op_fail(WSM_ERR_INVALID, "the scale must be finite");
+    const double factor = std::fabs((double)a->scale) * cache->k_scale * 1.44269504088896340736;   // of scores in base 2
+    if (factor > std::numeric_limits<float>::max())
+        return op_fail(WSM_ERR_INVALID, "the scale times the keys' scale, in base 2, is past fp32's range");
     if (a->batch == 0) return WSM_OK;
     const bool e8 = cache->dtype == WSM_DTYPE_E4M3;
     const bool join = attention_may_cut(max_tokens, a->window);
@@ -1040,8 +1044,8 @@ wsm_status wsm_paged_attention(const wsm_kv_cache *cache, const wsm_attention *a
     p.v_head = step_of(cache->v_strides[2], n_c[2]);
     p.table_stride = step_of(a->table_stride, a->batch);
     p.num_pages = cache->num_pages;
-    // (a scale of 0 would make NaN of what is masked; scores times this vanish next to one another all the same)
-    p.sl2 = std::max((float)(std::fabs((double)a->scale) * cache->k_scale * 1.44269504088896340736), 1e-37f);
+    // (a factor of 0 would make NaN of what is masked; fp32 scores times the least number above it all vanish)
+    p.sl2 = std::max((float)factor, std::numeric_limits<float>::denorm_min());
     p.negate = a->scale < 0.f;
     p.v_scale = cache->v_scale;
     p.batch = a->batch;
