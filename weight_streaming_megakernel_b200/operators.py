@@ -27,6 +27,8 @@ _E4M3 = torch.float8_e4m3fn
 _ROW_TYPES = (torch.bfloat16, torch.float16)
 _LOGIT_TYPES = (torch.float32, torch.bfloat16, torch.float16)
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_MOST_TOP = 32
+_MOST_INT = 2 ** 31 - 1
 
 # wsm_kv_cache, wsm_kv_rows, wsm_attention, wsm_experts, wsm_logprobs
 _CACHE = struct.Struct("@2P6qq4i2f")
@@ -201,6 +203,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if stream is not None or device != _current_device():
         return _elsewhere(paged_attention, device, stream, q, k_cache, v_cache, block_table, lengths, out, scale=scale,
                           window=window, k_scale=k_scale, v_scale=v_scale, lse=lse)
+    if window > _MOST_INT:
+        window = _MOST_INT                              # (more than any sequence)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         o0, o1 = heads * dim, dim
@@ -238,7 +242,7 @@ def expert_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: Opti
     gate and up rows in alternating blocks of 8 and y is [rows, N / 2] =
     silu(gate) * up.  row_scale: [rows] fp32 factors of the results (router
     weights).  Rows outside all experts are left as they were: in a new y
-    they are undefined.
+    they are undefined.  y shares no memory with x or w.
     """
     device = -1
     try:
@@ -287,7 +291,8 @@ def expert_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: Opti
 def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *, top: int = 0,
                    stream=None) -> TokenLogprobs:
     """Log probabilities of given tokens, the entropy of each row's
-    distribution and its `top` (at most 32) likeliest tokens.
+    distribution and its `top` (at most 32, and the vocabulary) likeliest
+    tokens.
 
     logits: [rows, vocab] fp32 (skinny_gemm's yf32), bf16 or fp16, rows any
     distance apart.  tokens: [rows] int64; a negative one asks for nothing and
@@ -311,13 +316,14 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
         _refuse(device, ("logits", logits, (None, None), _LOGIT_TYPES, False), *more)
     if stream is not None or device != _current_device():
         return _elsewhere(token_logprobs, device, stream, logits, tokens, top=top)
-    width = top if top > 0 else 0
+    width = top if 0 < top <= _MOST_TOP else 0          # (any other is refused below)
     logprob = logits.new_empty(rows, dtype=_F32)
     entropy = torch.empty_like(logprob)
     top_lp = logits.new_empty((rows, width), dtype=_F32)
     top_ids = logits.new_empty((rows, width), dtype=_I64)
     args = _LOGPROBS.pack(logits.data_ptr(), 0 if tokens is None else tokens.data_ptr(), logprob.data_ptr(),
-                          entropy.data_ptr(), top_ids.data_ptr(), top_lp.data_ptr(), x0, rows, vocab, top, _DTYPES[dtype])
+                          entropy.data_ptr(), top_ids.data_ptr(), top_lp.data_ptr(), x0, rows, vocab,
+                          min(top, _MOST_INT), _DTYPES[dtype])
     code = _wsm.lib().wsm_token_logprobs(args, _current_stream(device))
     if code:
         _wsm._check(code, "wsm_token_logprobs")
