@@ -37,7 +37,8 @@ constexpr int kAppendUnroll = 4;    // tokens in flight per thread
 // Reads a token's keys and values once and writes them once, 16 bytes a thread; nothing to compute but the 8-bit
 // rounding.  On a B200: 64 tokens of 8 heads of 128, 2.1 us (a launch; the call costs its host 5.9); 16001 tokens
 // 24.1 us, 131 MB at 5.4 TB/s, the floor at copy speed 20.4: a page's rows are 256 bytes in one place each, and two or
-// eight tokens' loads in flight instead of four took 25.6 and 30 us.
+// eight tokens' loads in flight instead of four took 25.6 and 30 us.  Into an 8-bit cache 32 us, 98 MB (15.3): a
+// division and a rounding to every element come on top, and stores of 8 bytes.
 //
 // One thread moves the same 8-element chunk (16 bytes) of many tokens: its place within a token is worked
 // out once, and kAppendUnroll tokens' loads are in flight before the first store.
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // do not depend on timing.
 //
 // Measured on a B200 (floor: the cache's bytes at the 6440 GB/s of a copy): one token over 131041 of a 16-bit cache of
-// 8 heads of 128 101 to 106 us (floor 83); 64 ragged sequences of up to 4000 tokens 36 to 42 us (22); 96 over an 8-bit cache
+// 8 heads of 128 101 to 107 us (floor 83); 64 ragged sequences of up to 4000 tokens 36 to 42 us (22); 96 over an 8-bit cache
 // 53 to 60 us (34): the warps issue in 54 % of the cycles and the cache comes at 4.2 TB/s; one sequence of 37 tokens
 // 7.0 us.  About 4.5 us of each is the chain of reads that finds a warp its first tokens (lengths, then the table, then
 // keys), 5 to 6 the join's, which reads its items' places as the main kernel left them.  (Every block of the join

@@ -19,10 +19,10 @@
 //   depend on which SM ran what.
 //
 // Measured on a B200 (floors: weights at the 6440 GB/s of a copy, products at cuBLAS' 1.67 PFLOP/s, 1.39 sustained): 16
-// rows over 32 experts of 4096 x 4096, 65 to 71 us by which experts get them (66: weights at 5.6 to 6.2 TB/s, the
+// rows over 32 experts of 4096 x 4096, 62 to 71 us by which experts get them (66: weights at 5.6 to 6.2 TB/s, the
 // tensor pipe 4 % busy); 1000 rows over 64 experts of 4096 x 1280, 101 to 109 us (106 were all to get rows); 8192 rows
-// over 16 experts of 6144 x 4096, 395 us in a burst and 455 in a loop, where the power leaves 1.3 to 1.4 GHz (246,
-// 296).  There some 43 KB a stage come out of L2 at 60 bytes a clock, about what an SM takes in: 550 thousand clocks,
+// over 16 experts of 6144 x 4096, 360 to 395 us in a burst and 410 to 480 in a loop, where the power leaves 1.3 to 1.4
+// GHz (246, 296), with the tensor pipe 61 % busy.  There some 43 KB a stage come out of L2 at 60 bytes a clock, about what an SM takes in: 550 thousand clocks,
 // as many without the products, and 370 without the copies.  CTA pairs (cta_group::2) load 30 % less and took 8 %
 // less time there, but as much or 4 % more at 3000 to 8192 rows over smaller experts and 117 to 128 us on the 1000
 // rows: half as many tiles are in flight.
@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(kMaxExperts) experts_plan_kernel(const __grid_
     if (have && (raw != hi || (e == 0 && raw0 != lo0))) record_op_error(&g_experts_error, e, kSiteOffsets);
     const int m = have ? hi - lo : 0;
     // The highest tiles read the least (for 256 rows of X 48 KB to a K box, for 64 24 KB), but a call with few of them
-    // leaves SMs without: below one to three SMs, lower ones.  (On a B200, 400 rows of 4 experts of 1152 x 3944: 38 us
-    // in tiles of up to 256 rows, 26 of 128; 1652 of 15 experts of 304 x 904: 17.5 and 15.4; 300 rows of one expert of
-    // 4096 x 4096, 64 tiles, stay with 256: 29 us, 33 in tiles of 128.)
+    // leaves SMs without: below one to three SMs, lower ones.  (On a B200, 400 rows of 4 experts of 1152 x 3944: 27.8
+    // us in tiles of up to 256 rows, 25.6 of 128; 1652 of 15 experts of 304 x 904: 16.5 and 14.6; 300 rows of one expert of
+    // 4096 x 4096, 64 tiles, stay with 256: 27 us.)
     int rows_log = kTileRowsLog, mt, tiles, tile_end, total;
     for (;; --rows_log) {
         mt = m_tiles_of(m, rows_log);
@@ -279,9 +279,9 @@ __device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap *
         : "memory");
 }
 
-// z / (1 + e^-z) * up by the hardware's exponential and division, relative error about 2^-20 (below z = -87, where
-// the value is under 2^-119, it is 0): the outputs are rounded to 2^-11 at the finest, and there are as many of
-// these as outputs.
+// z / (1 + e^-z) * up by the hardware's exponential and division, relative error about 2^-20 up to |z| = 16, growing with
+// the exponent's argument to 2^-17.5 at z = -87 (below that, where the value is under 2^-119, it is 0): the outputs are
+// rounded to 2^-11 at the finest, and there are as many of these as outputs.
 __device__ __forceinline__ float silu_mul(float z, float up) { return __fdividef(z, 1.f + __expf(-z)) * up; }
 
 // Where outputs go: the launch's parameters, which the epilogue keeps in registers (read in its loop, they are

@@ -17,7 +17,7 @@
 // to eight, whose parts meet in the first one's shared memory: no scratch and one launch.
 //
 // Measured on a B200: 2049 rows of 100003 fp32 126 to 136 us, 6.0 to 6.5 TB/s (a copy moves 6.44); 128 rows of
-// 128000 bf16, 20 alternatives, 16.5 us (floor 5.1) and 4 rows of 131072 fp32, 8 alternatives, 9.0 us (0.3): a read's
+// 128000 bf16, 20 alternatives, 17 us (floor 5.1) and 4 rows of 131072 fp32, 8 alternatives, 8.5 to 9 us (0.3): a read's
 // latency, the pass, then some 3 us to find and rank the alternatives.
 #include "wsm_ops.cuh"
 
