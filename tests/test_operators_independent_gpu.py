@@ -110,13 +110,16 @@ def test_independent_call_that_allocates_its_output_waits():
     first = wsm.skinny_gemm(x, w)
     seen = torch.empty(want.shape, dtype=want.dtype, pin_memory=True)
     side = torch.cuda.Stream()
-    old = torch.full_like(want, 3.0)
+    pool = torch.cuda.MemPool()
+    with torch.cuda.use_mem_pool(pool):                 # (of its own, so that the dropped tensor's block is the one there is)
+        old = torch.full_like(want, 3.0)
     at = old.data_ptr()
     torch.cuda.synchronize()
     wsm.debug_stall(1, 1_000_000_000)
     wsm.skinny_gemm(x, w, first)
     del old
-    y = wsm.skinny_gemm(x, w, flags=IND)
+    with torch.cuda.use_mem_pool(pool):
+        y = wsm.skinny_gemm(x, w, flags=IND)
     assert y.data_ptr() == at
     time.sleep(0.2)
     with torch.cuda.stream(side):

@@ -246,9 +246,11 @@ def skinny_gemm(x: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor] = No
     """Y = X @ W.T on the current (or given) stream; returns Y.  With
     epilogue=EPI_SILU_MUL, W is the fused gate+up weight (rows interleaved in
     blocks of 8) and Y is [M, N/2] = silu(gate) * up; with EPI_RESIDUAL,
-    Y = X @ W.T + r.  With FLAG_INDEPENDENT give y: a y allocated here may be
-    memory that calls queued before still read, so the call then starts after
-    them (and runs beside those that follow)."""
+    Y = X @ W.T + r.  With FLAG_INDEPENDENT give a y (and yf32) allocated
+    before the calls that this one may run beside: memory that the allocator
+    hands out later may be that of a tensor dropped since, which they still
+    read or write.  Without y the call starts after them, and runs beside
+    those that follow."""
     _check_operand("x", x)
     _check_operand("w", w)
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
